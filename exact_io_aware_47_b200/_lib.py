@@ -26,8 +26,14 @@ FA_ERR_DEVICE_SCALE = 11
 FA_BF16 = 0
 FA_FP16 = 1
 
+FA_CACHE_16 = 0
+FA_CACHE_E4M3 = 1
+
 # exported symbol -> (restype, argtypes)
 _VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_I64 = ctypes.c_int64
+_ROPE = (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _I, _VP, _I64, _VP, _I, _I, _I, _I, _I,
+              _F, _I, _VP])
 SIGNATURES = {
     "fa_fwd": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _VP, _I, _VP]),
     "fa_bwd_workspace_size": (_SZ, [_I, _I, _I, _I]),
@@ -56,6 +62,15 @@ SIGNATURES = {
     "fa_quantize_e4m3": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _I, _VP]),
     "fa_fwd_e4m3": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _VP, _I,
                          _VP]),
+    "fa_rope": _ROPE,
+    "fa_rope_bwd": _ROPE,
+    "fa_cache_write": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I,
+                            _I, _I, _I, _I, _I, _VP]),
+    "fa_cache_read": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I,
+                           _I, _I, _VP]),
+    "fa_fwd_tree_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "fa_fwd_tree": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _I, _VP, _VP, _VP, _I,
+                         _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _VP]),
     "fa_set_wait_limit_ns": (ctypes.c_ulonglong, [ctypes.c_ulonglong]),
     "fa_device_status": (_I, [_VP, ctypes.POINTER(ctypes.c_uint32)]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
@@ -185,6 +200,30 @@ def fa_fwd_e4m3(q8, k8, v8, q_descale, k_descale, v_descale, o, lse, B, H, N, d,
                 seqlens, out_dtype, stream):
     return load().fa_fwd_e4m3(q8, k8, v8, q_descale, k_descale, v_descale, o, lse, B, H, N, d,
                               scale, causal, seqlens, out_dtype, stream)
+
+
+def fa_rope(*args):
+    return load().fa_rope(*args)
+
+
+def fa_rope_bwd(*args):
+    return load().fa_rope_bwd(*args)
+
+
+def fa_cache_write(*args):
+    return load().fa_cache_write(*args)
+
+
+def fa_cache_read(*args):
+    return load().fa_cache_read(*args)
+
+
+def fa_fwd_tree_workspace_size(B, Hq, Hk, T, d):
+    return load().fa_fwd_tree_workspace_size(B, Hq, Hk, T, d)
+
+
+def fa_fwd_tree(*args):
+    return load().fa_fwd_tree(*args)
 
 
 def fa_bwd_noalloc_max_bytes():

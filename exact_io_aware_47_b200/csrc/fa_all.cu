@@ -4,3 +4,7 @@
 #include "fa_fwd.cu"
 #include "fa_bwd.cu"
 #include "fa_quant.cu"
+#include "fa_rope.cu"
+#include "fa_cache.cu"
+#include "fa_tree.cu"
+#include "fa_serve_api.cu"

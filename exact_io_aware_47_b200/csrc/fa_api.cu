@@ -656,8 +656,8 @@ extern "C" const char* fa_status_string(int status) {
     case FA_ERR_ARCH: return "current device is not sm_100 (B200)";
     case FA_ERR_CUDA: return "CUDA call or launch failed";
     case FA_ERR_DEVICE_TIMEOUT: return "device pipeline wait timed out";
-    case FA_ERR_DEVICE_SEQLEN: return "seqlens value outside [1, N] (clamped on device)";
-    case FA_ERR_WORKSPACE: return "backward workspace missing or too small";
+    case FA_ERR_DEVICE_SEQLEN: return "sequence length, position or page out of range (clamped or skipped on device)";
+    case FA_ERR_WORKSPACE: return "workspace missing or too small";
     case FA_ERR_DEVICE_LAYOUT: return "kernel refused: shared-memory window misaligned";
     case FA_ERR_SCRATCH_LIMIT:
       return "problem needs more backward scratch than fa_bwd_noalloc's static array holds";

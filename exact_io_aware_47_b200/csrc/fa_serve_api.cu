@@ -1,0 +1,287 @@
+// C ABI of the serving operators: argument checks and launches.
+//
+// As in fa_api.cu, every check runs on the host before anything is enqueued.
+#include "fa_serve.h"
+
+namespace fa {
+namespace {
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// Strides of a [B, H, N, d] tensor: host int64[3] or nullptr for contiguous.
+int read_strides(const int64_t* s, int H, int N, int d, Strides3* out) {
+  if (s == nullptr) {
+    *out = Strides3{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
+    return FA_OK;
+  }
+  for (int i = 0; i < 3; ++i)
+    if (s[i] < 0 || s[i] > (1ll << 40)) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (s[i] % 8 != 0) return FA_ERR_ALIGNMENT;
+  *out = Strides3{s[0], s[1], s[2]};
+  return FA_OK;
+}
+
+// Elements from the first to one past the last.
+long long extent(const Strides3& s, int B, int H, int N, int d) {
+  return (B - 1) * s.b + (H - 1) * s.h + (N - 1) * s.n + d;
+}
+
+// Whether rows of a strided tensor can share memory.  With the dimensions of
+// more than one element sorted by stride, each stride has to reach past all
+// that the smaller ones span.
+bool rows_may_overlap(const Strides3& s, int B, int H, int N, int d) {
+  long long st[3] = {s.b, s.h, s.n};
+  long long n[3] = {B, H, N};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (st[j] > st[j + 1]) {
+        std::swap(st[j], st[j + 1]);
+        std::swap(n[j], n[j + 1]);
+      }
+  long long span = d;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (st[i] < span) return true;
+    span += (n[i] - 1) * st[i];
+  }
+  return false;
+}
+
+bool same_view(const void* x, const Strides3& xs, const void* y, const Strides3& ys, int B, int H,
+               int N) {
+  return x == y && (B == 1 || xs.b == ys.b) && (H == 1 || xs.h == ys.h) && (N == 1 || xs.n == ys.n);
+}
+
+bool ranges_overlap(const void* x, long long nx, const void* y, long long ny) {
+  const uint8_t* a = static_cast<const uint8_t*>(x);
+  const uint8_t* b = static_cast<const uint8_t*>(y);
+  return a < b + 2 * ny && b < a + 2 * nx;
+}
+
+int rope_tensor(const void* x, const int64_t* xs, void* y, const int64_t* ys, int B, int H, int N,
+                int d, int dtype, RopeTensor* t) {
+  if (!x || !y) return FA_ERR_INVALID_ARG;
+  int st = check_common(B, H, N, d, 1.f, dtype);
+  if (st != FA_OK) return st;
+  if (!aligned(x, 16) || !aligned(y, 16)) return FA_ERR_ALIGNMENT;
+  t->x = static_cast<const uint8_t*>(x);
+  t->y = static_cast<uint8_t*>(y);
+  t->heads = H;
+  if ((st = read_strides(xs, H, N, d, &t->xs)) != FA_OK) return st;
+  if ((st = read_strides(ys, H, N, d, &t->ys)) != FA_OK) return st;
+  if (rows_may_overlap(t->ys, B, H, N, d)) return FA_ERR_INVALID_ARG;
+  t->in_place = same_view(x, t->xs, y, t->ys, B, H, N);
+  if (!t->in_place &&
+      ranges_overlap(x, extent(t->xs, B, H, N, d), y, extent(t->ys, B, H, N, d)))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+int rope_core(const void* q, const int64_t* qs, void* qo, const int64_t* qos, int Hq,
+              const void* k, const int64_t* ks, void* ko, const int64_t* kos, int Hk,
+              const int32_t* positions, int64_t positions_stride, const double* inv_freq, int B,
+              int N, int d, int rot, int interleaved, float factor, int dtype, float sign,
+              void* stream) {
+  if (!inv_freq || positions_stride < 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(factor) && factor > 0.f)) return FA_ERR_INVALID_ARG;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  int st = rope_tensor(q, qs, qo, qos, B, Hq, N, d, dtype, &p.t[0]);
+  if (st != FA_OK) return st;
+  if (k == nullptr) {
+    if (Hk != 0 || ko != nullptr) return FA_ERR_INVALID_ARG;
+  } else {
+    st = rope_tensor(k, ks, ko, kos, B, Hk, N, d, dtype, &p.t[1]);
+    if (st != FA_OK) return st;
+    if (qo == ko || static_cast<const void*>(qo) == k || static_cast<const void*>(ko) == q)
+      return FA_ERR_INVALID_ARG;
+  }
+  if (rot < 16 || rot > d || rot % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if ((positions && !aligned(positions, 4)) || !aligned(inv_freq, 8)) return FA_ERR_ALIGNMENT;
+  p.positions = positions;
+  p.pos_stride = positions_stride;
+  p.inv_freq = inv_freq;
+  p.B = B;
+  p.N = N;
+  p.rot = rot;
+  p.factor = factor;
+  p.sign = sign;
+  DeviceInfo di;
+  st = current_device_info(&di);
+  if (st != FA_OK) return st;
+  const cudaError_t e = launch_rope(d, dtype == FA_BF16, interleaved != 0, p, di.num_sms,
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Checks shared by everything that takes a cache; fills the view.
+int cache_view(const void* k_cache, const void* v_cache, const float* k_scale,
+               const float* v_scale, const int32_t* table, int table_stride, int B, int Hk, int d,
+               int num_pages, int page_size, int format, CacheView* c) {
+  if (!k_cache || !v_cache || k_cache == v_cache) return FA_ERR_INVALID_ARG;
+  if (format != FA_CACHE_16 && format != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
+  if (format == FA_CACHE_E4M3 && (!k_scale || !v_scale || k_scale == v_scale))
+    return FA_ERR_INVALID_ARG;
+  if (Hk < 1 || num_pages < 1 || page_size < 1) return FA_ERR_INVALID_ARG;
+  if (table ? table_stride < 1 : num_pages < B) return FA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0 || static_cast<long long>(num_pages) * Hk >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || (table && !aligned(table, 4)) ||
+      (format == FA_CACHE_E4M3 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
+    return FA_ERR_ALIGNMENT;
+  c->k = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+  c->v = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+  c->k_scale = const_cast<float*>(k_scale);
+  c->v_scale = const_cast<float*>(v_scale);
+  c->table = table;
+  c->table_stride = table ? table_stride : 1;
+  c->num_pages = num_pages;
+  c->page_size = page_size;
+  c->Hk = Hk;
+  return FA_OK;
+}
+
+// Query rows of one K/V head are cut into tiles of at most this many.
+int check_tree(int B, int Hq, int Hk, int T, int d, float scale, int dtype) {
+  const int st = check_common(B, Hq, T, d, scale, dtype);
+  if (st != FA_OK) return st;
+  if (Hk < 1 || Hq % Hk != 0) return FA_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(Hq / Hk) * T;
+  if (static_cast<long long>(B) * Hk * ((rows + 15) / 16) >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" int fa_rope(const void* q, const int64_t* q_strides, void* q_out,
+                       const int64_t* q_out_strides, int Hq, const void* k,
+                       const int64_t* k_strides, void* k_out, const int64_t* k_out_strides, int Hk,
+                       const int32_t* positions, int64_t positions_stride, const double* inv_freq,
+                       int B, int N, int d, int rot, int interleaved, float factor, int dtype,
+                       void* stream) {
+  return rope_core(q, q_strides, q_out, q_out_strides, Hq, k, k_strides, k_out, k_out_strides, Hk,
+                   positions, positions_stride, inv_freq, B, N, d, rot, interleaved, factor, dtype,
+                   1.f, stream);
+}
+
+extern "C" int fa_rope_bwd(const void* dq, const int64_t* dq_strides, void* dq_in,
+                           const int64_t* dq_in_strides, int Hq, const void* dk,
+                           const int64_t* dk_strides, void* dk_in, const int64_t* dk_in_strides,
+                           int Hk, const int32_t* positions, int64_t positions_stride,
+                           const double* inv_freq, int B, int N, int d, int rot, int interleaved,
+                           float factor, int dtype, void* stream) {
+  return rope_core(dq, dq_strides, dq_in, dq_in_strides, Hq, dk, dk_strides, dk_in, dk_in_strides,
+                   Hk, positions, positions_stride, inv_freq, B, N, d, rot, interleaved, factor,
+                   dtype, -1.f, stream);
+}
+
+extern "C" int fa_cache_write(const void* k, const int64_t* k_strides, const void* v,
+                              const int64_t* v_strides, void* k_cache, void* v_cache,
+                              float* k_scale, float* v_scale, const int32_t* block_table,
+                              int table_stride, const int32_t* start, const int32_t* lens, int B,
+                              int Hk, int N, int d, int num_pages, int page_size, int format,
+                              int dtype, void* stream) {
+  if (!k || !v) return FA_ERR_INVALID_ARG;
+  int st = check_common(B, Hk, N, d, 1.f, dtype);
+  if (st != FA_OK) return st;
+  CacheCopyParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = cache_view(k_cache, v_cache, k_scale, v_scale, block_table, table_stride, B, Hk, d,
+                  num_pages, page_size, format, &p.c);
+  if (st != FA_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16) || (start && !aligned(start, 4)) ||
+      (lens && !aligned(lens, 4)))
+    return FA_ERR_ALIGNMENT;
+  if ((st = read_strides(k_strides, Hk, N, d, &p.ks)) != FA_OK) return st;
+  if ((st = read_strides(v_strides, Hk, N, d, &p.vs)) != FA_OK) return st;
+  p.k = static_cast<const uint8_t*>(k);
+  p.v = static_cast<const uint8_t*>(v);
+  p.start = start;
+  p.lens = lens;
+  p.B = B;
+  p.N = N;
+  DeviceInfo di;
+  st = current_device_info(&di);
+  if (st != FA_OK) return st;
+  const cudaError_t e = launch_cache_write(d, dtype == FA_BF16, format == FA_CACHE_E4M3, p,
+                                           static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" int fa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, void* k_out, void* v_out,
+                             const int32_t* block_table, int table_stride, const int32_t* start,
+                             const int32_t* lens, int B, int Hk, int N, int d, int num_pages,
+                             int page_size, int format, int dtype, void* stream) {
+  if (!k_out || !v_out || k_out == v_out) return FA_ERR_INVALID_ARG;
+  int st = check_common(B, Hk, N, d, 1.f, dtype);
+  if (st != FA_OK) return st;
+  CacheCopyParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = cache_view(k_cache, v_cache, k_scale, v_scale, block_table, table_stride, B, Hk, d,
+                  num_pages, page_size, format, &p.c);
+  if (st != FA_OK) return st;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || (start && !aligned(start, 4)) ||
+      (lens && !aligned(lens, 4)))
+    return FA_ERR_ALIGNMENT;
+  p.k_out = static_cast<uint8_t*>(k_out);
+  p.v_out = static_cast<uint8_t*>(v_out);
+  p.start = start;
+  p.lens = lens;
+  p.B = B;
+  p.N = N;
+  DeviceInfo di;
+  st = current_device_info(&di);
+  if (st != FA_OK) return st;
+  const cudaError_t e = launch_cache_read(d, dtype == FA_BF16, format == FA_CACHE_E4M3, p,
+                                          static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" size_t fa_fwd_tree_workspace_size(int B, int Hq, int Hk, int T, int d) {
+  if (check_tree(B, Hq, Hk, T, d, 1.f, FA_BF16) != FA_OK) return 0;
+  return 256;
+}
+
+extern "C" int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale, void* o, float* lse,
+                           void* workspace, size_t workspace_bytes, const int32_t* block_table,
+                           int table_stride, const int32_t* ctx_lens, const int32_t* draft_lens,
+                           const uint8_t* tree_mask, int mask_per_batch, int B, int Hq, int Hk,
+                           int T, int d, int num_pages, int page_size, float scale, int format,
+                           int dtype, void* stream) {
+  if (!q || !o || !lse || !ctx_lens) return FA_ERR_INVALID_ARG;
+  int st = check_tree(B, Hq, Hk, T, d, scale, dtype);
+  if (st != FA_OK) return st;
+  TreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = cache_view(k_cache, v_cache, k_scale, v_scale, block_table, table_stride, B, Hk, d,
+                  num_pages, page_size, format, &p.c);
+  if (st != FA_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(ctx_lens, 4) ||
+      (draft_lens && !aligned(draft_lens, 4)))
+    return FA_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < fa_fwd_tree_workspace_size(B, Hq, Hk, T, d))
+    return FA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return FA_ERR_ALIGNMENT;
+  p.q = static_cast<const uint8_t*>(q);
+  p.o = static_cast<uint8_t*>(o);
+  p.lse = lse;
+  p.ctx_lens = ctx_lens;
+  p.draft_lens = draft_lens;
+  p.mask = tree_mask;
+  p.mask_stride = mask_per_batch ? static_cast<long long>(T) * T : 0;
+  p.B = B;
+  p.Hq = Hq;
+  p.T = T;
+  p.group = Hq / Hk;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  DeviceInfo di;
+  st = current_device_info(&di);
+  if (st != FA_OK) return st;
+  const cudaError_t e = launch_tree(d, dtype == FA_BF16, format == FA_CACHE_E4M3, p,
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}

@@ -65,8 +65,8 @@ typedef enum {
   FA_ERR_ARCH = 4,            /* current device is not an sm_100 (B200) GPU     */
   FA_ERR_CUDA = 5,            /* a CUDA runtime/driver call or launch failed    */
   FA_ERR_DEVICE_TIMEOUT = 6,  /* device: a pipeline wait gave up (fa_device_status) */
-  FA_ERR_DEVICE_SEQLEN = 7,   /* device: seqlens[b] outside [1, N] (fa_device_status) */
-  FA_ERR_WORKSPACE = 8,       /* backward workspace missing or too small        */
+  FA_ERR_DEVICE_SEQLEN = 7,   /* device: a length, position or page out of range (fa_device_status) */
+  FA_ERR_WORKSPACE = 8,       /* workspace missing or too small                 */
   FA_ERR_DEVICE_LAYOUT = 9,   /* device: shared-memory window misaligned, kernel refused (fa_device_status) */
   FA_ERR_SCRATCH_LIMIT = 10,  /* fa_bwd_noalloc: workspace would exceed its static array */
   FA_ERR_DEVICE_SCALE = 11    /* device: e4m3 descale not finite and > 0, or infinite or NaN
@@ -302,6 +302,122 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
 
 /* Size in bytes of the static workspace fa_bwd_noalloc uses. */
 size_t fa_bwd_noalloc_max_bytes(void);
+
+/*
+ * Serving: rotary positions, a paged K/V cache that can hold 8-bit rows, and
+ * attention of drafted tokens over it.  Together they form one decoding step:
+ * fa_rope on the new Q and K, fa_cache_write of the new K and V, fa_fwd_tree
+ * of the new Q over the cache.  fa_cache_read gives a cached prefix back in
+ * 16 bits, for fa_fwd; fa_rope and fa_rope_bwd also frame fa_fwd and fa_bwd in
+ * training.  Conventions (memory, streams, errors) as above.
+ *
+ * Rotary positions.  Row n of batch b of x [B, H, N, d] is rotated pair by
+ * pair by the angle of its position p: for i < rot / 2,
+ *     theta_i = p * inv_freq[i]                    (64 bits)
+ *     y_a = factor (x_a cos theta_i - x_b sin theta_i)
+ *     y_b = factor (x_b cos theta_i + x_a sin theta_i)
+ *   with (a, b) = (2 i, 2 i + 1) if interleaved, (i, i + rot / 2) otherwise;
+ *   columns rot .. d - 1 are copied.  The sums run in fp32 and are rounded once.
+ *   fa_rope_bwd is the gradient: dx from dy, the same with -theta.
+ *   q, k: two tensors of B, N, d rotated by one launch, with Hq and Hk heads;
+ *     k may be NULL with Hk = 0.  *_strides: three host int64 (batch, head,
+ *     row) in elements, each >= 0 and a multiple of 8, NULL for contiguous [B, H, N, d]; d
+ *     is contiguous.  Two rows of an output must not share memory.  An output
+ *     is its input (same pointer and strides) or overlaps neither input.
+ *   positions: device int32; row n of batch b is at
+ *     positions[b * positions_stride + n] (positions_stride >= 0; 0: shared
+ *     by the batch); NULL: p = n.  Any int32 value, in any order.
+ *   inv_freq: device double [rot / 2], 8-byte aligned.  rot: a multiple of 16
+ *     with 16 <= rot <= d.  factor finite and > 0.
+ *   B*H*N*d < 2^31 for both tensors; d in {64, 128}.
+ */
+int fa_rope(const void* q, const int64_t* q_strides, void* q_out, const int64_t* q_out_strides,
+            int Hq, const void* k, const int64_t* k_strides, void* k_out,
+            const int64_t* k_out_strides, int Hk, const int32_t* positions,
+            int64_t positions_stride, const double* inv_freq, int B, int N, int d, int rot,
+            int interleaved, float factor, int dtype, void* stream);
+int fa_rope_bwd(const void* dq, const int64_t* dq_strides, void* dq_in,
+                const int64_t* dq_in_strides, int Hq, const void* dk, const int64_t* dk_strides,
+                void* dk_in, const int64_t* dk_in_strides, int Hk, const int32_t* positions,
+                int64_t positions_stride, const double* inv_freq, int B, int N, int d, int rot,
+                int interleaved, float factor, int dtype, void* stream);
+
+/*
+ * The K/V cache.  A pool of pages, each holding page_size consecutive
+ * positions of one sequence for every K/V head:
+ *   k_cache, v_cache [num_pages, Hk, page_size, d], in one of two formats:
+ *     FA_CACHE_16    16-bit values of `dtype`; the scale pointers are unused
+ *     FA_CACHE_E4M3  e4m3 codes, and k_scale, v_scale [num_pages, Hk,
+ *                    page_size] float32: a row stands for code * scale
+ *   page_size: a multiple of 16.  num_pages * Hk < 2^31; the caches may be
+ *     larger than 2^32 bytes.
+ *   block_table: device int32 [B, table_stride]: position j of sequence b is
+ *     row j % page_size of page block_table[b * table_stride + j / page_size],
+ *     for j < table_stride * page_size.  NULL: sequence b has page b alone
+ *     (num_pages >= B), i.e. the cache is [B, Hk, page_size, d].  Sequences
+ *     may share pages that are only read.
+ *   Positions past the table, pages outside [0, num_pages) and lengths out of
+ *   range are reported by fa_device_status() as FA_ERR_DEVICE_SEQLEN; nothing
+ *   outside the buffers is read or written.
+ *
+ * fa_cache_write: row n of k, v [B, Hk, N, d] (16-bit, `dtype`, strides as in
+ *   fa_rope) goes to position start[b] + n, for n < lens[b] (lens NULL: N).
+ *   start NULL: 0.  The slots written by one call must be distinct.
+ *   e4m3: per row, amax = max |x|, top = max(amax, 448 * 2^-126),
+ *     scale = top / 448 (1 for a row of zeros) and code = e4m3(x * (448 / top)),
+ *     in fp32 and rounded as by fa_quantize_e4m3.  A row with an infinite or
+ *     NaN value gets the scale NaN (it reads back as NaN) and is reported as
+ *     FA_ERR_DEVICE_SCALE.  Other rows of the cache stay as they were.
+ * fa_cache_read: position start[b] + n to row n of k_out, v_out [B, Hk, N, d]
+ *   (contiguous, 16-bit, `dtype`) for n < lens[b]: code * scale in fp32,
+ *   rounded once.  Rows behind lens[b], and rows of bad positions, stay as
+ *   they were.
+ *   0 <= lens[b] <= N is required.  B*Hk*N*d < 2^31; d in {64, 128}.
+ */
+typedef enum { FA_CACHE_16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_format;
+
+int fa_cache_write(const void* k, const int64_t* k_strides, const void* v,
+                   const int64_t* v_strides, void* k_cache, void* v_cache, float* k_scale,
+                   float* v_scale, const int32_t* block_table, int table_stride,
+                   const int32_t* start, const int32_t* lens, int B, int Hk, int N, int d,
+                   int num_pages, int page_size, int format, int dtype, void* stream);
+int fa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                  const float* v_scale, void* k_out, void* v_out, const int32_t* block_table,
+                  int table_stride, const int32_t* start, const int32_t* lens, int B, int Hk,
+                  int N, int d, int num_pages, int page_size, int format, int dtype,
+                  void* stream);
+
+/*
+ * Attention of drafted tokens over the cache (T = 1: ordinary decoding).
+ * Sequence b has ctx_lens[b] positions of context in the cache, followed by
+ * its drafted tokens' rows: token u is at position ctx_lens[b] + u.
+ *   q [B, Hq, T, d] 16-bit, contiguous; out o (as q) and lse [B, Hq, T].
+ *   Shared K/V heads: Hq is a multiple of Hk; query head h reads K/V head
+ *     h / (Hq / Hk).
+ *   Query t of sequence b sees every key of the context, and the key of
+ *     drafted token u < n_b if tree_mask[(b *) T * T + t * T + u] != 0
+ *     (tree_mask NULL: u <= t, a chain).  n_b = draft_lens[b] (NULL: T).
+ *     tree_mask: device uint8 [T, T], or [B, T, T] if mask_per_batch != 0.
+ *   Keys that a query does not see add nothing to its result, whatever their
+ *     rows hold (infinities and NaN too).  A query that sees no key (or only
+ *     scores of minus infinity) gets O = 0 and LSE = -inf.  Rows t >= n_b of o
+ *     and lse stay as they were.
+ *   0 <= draft_lens[b] <= T and 0 <= ctx_lens[b] with ctx_lens[b] + n_b within
+ *     the table are required; other values are clamped and reported.  With a
+ *     bad page the results of its sequences are unspecified.
+ *   workspace: fa_fwd_tree_workspace_size(B, Hq, Hk, T, d) bytes, 256-byte
+ *     aligned; its contents on entry do not matter.  Calls that may overlap on
+ *     the GPU need one each.
+ *   Results do not depend on the order in which the GPU runs the work.
+ *   B*Hq*T*d < 2^31, B*Hk*ceil(Hq/Hk*T / 16) < 2^31; d in {64, 128}.
+ */
+size_t fa_fwd_tree_workspace_size(int B, int Hq, int Hk, int T, int d);
+int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                const float* v_scale, void* o, float* lse, void* workspace,
+                size_t workspace_bytes, const int32_t* block_table, int table_stride,
+                const int32_t* ctx_lens, const int32_t* draft_lens, const uint8_t* tree_mask,
+                int mask_per_batch, int B, int Hq, int Hk, int T, int d, int num_pages,
+                int page_size, float scale, int format, int dtype, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of
