@@ -76,7 +76,18 @@ struct TreeParams {
   long long mask_stride;     // T * T, or 0 for a shared mask
   int B, Hq, T, group;       // group = Hq / Hk
   float scale_log2;          // scale * log2(e)
+  int row_tiles;             // ceil(group * T / rows of a tile)
+  int box;                   // keys of one TMA load: a power of two that divides page_size
+  int grid;                  // CTAs
+  int* heads;                // workspace: [grid][4], see fa_tree_kernel
+  float* partial;            // workspace: [grid][2] slots
+  unsigned long long wait_ns;
 };
+
+constexpr int kTreeMaxCtas = 160;
+
+// Rows of a tile, for `rows` query rows per K/V head.
+inline int tree_rows(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 cudaError_t launch_rope(int d, bool bf16, bool interleaved, const RopeParams& p, int num_sms,
                         cudaStream_t stream);
@@ -84,6 +95,7 @@ cudaError_t launch_cache_write(int d, bool bf16, bool e4m3, const CacheCopyParam
                                cudaStream_t stream);
 cudaError_t launch_cache_read(int d, bool bf16, bool e4m3, const CacheCopyParams& p,
                               cudaStream_t stream);
-cudaError_t launch_tree(int d, bool bf16, bool e4m3, const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_tree(int d, bool bf16, bool e4m3, int rows, const CUtensorMap& tmk,
+                        const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream);
 
 }  // namespace fa

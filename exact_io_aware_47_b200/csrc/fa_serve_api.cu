@@ -128,7 +128,7 @@ int cache_view(const void* k_cache, const void* v_cache, const float* k_scale,
   if (page_size % 16 != 0 || static_cast<long long>(num_pages) * Hk >= (1ll << 31))
     return FA_ERR_UNSUPPORTED;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || (table && !aligned(table, 4)) ||
-      (format == FA_CACHE_E4M3 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
+      (format == FA_CACHE_E4M3 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
     return FA_ERR_ALIGNMENT;
   c->k = static_cast<uint8_t*>(const_cast<void*>(k_cache));
   c->v = static_cast<uint8_t*>(const_cast<void*>(v_cache));
@@ -142,7 +142,27 @@ int cache_view(const void* k_cache, const void* v_cache, const float* k_scale,
   return FA_OK;
 }
 
-// Query rows of one K/V head are cut into tiles of at most this many.
+// [num_pages * Hk, page_size, d] view of a cache; box = 128 bytes x box rows,
+// 128-byte swizzle.  e4m3 rows of d = 64 are filled with zeros to 128 bytes.
+int make_map_cache(CUtensorMap* map, const void* ptr, const CacheView& c, int d, int box_rows,
+                   int format, int dtype) {
+  const bool e4m3 = format == FA_CACHE_E4M3;
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * (e4m3 ? 1 : 2);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.num_pages) * c.Hk};
+  const cuuint64_t strides[2] = {row, row * c.page_size};
+  const cuuint32_t box[3] = {e4m3 ? 128u : 64u, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map,
+                              e4m3               ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                              : dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              3, const_cast<void*>(ptr), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 int check_tree(int B, int Hq, int Hk, int T, int d, float scale, int dtype) {
   const int st = check_common(B, Hq, T, d, scale, dtype);
   if (st != FA_OK) return st;
@@ -242,7 +262,10 @@ extern "C" int fa_cache_read(const void* k_cache, const void* v_cache, const flo
 
 extern "C" size_t fa_fwd_tree_workspace_size(int B, int Hq, int Hk, int T, int d) {
   if (check_tree(B, Hq, Hk, T, d, 1.f, FA_BF16) != FA_OK) return 0;
-  return 256;
+  // per CTA: what it continues (4 ints) and two partial results of a tile's
+  // rows (fp32 O, reference and sum)
+  const size_t slot = static_cast<size_t>(tree_rows(static_cast<long long>(Hq / Hk) * T)) * (d + 2) * sizeof(float);
+  return round256(kTreeMaxCtas * 4 * sizeof(int)) + round256(kTreeMaxCtas * 2 * slot);
 }
 
 extern "C" int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -278,10 +301,27 @@ extern "C" int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cac
   p.T = T;
   p.group = Hq / Hk;
   p.scale_log2 = scale * 1.4426950408889634f;
+  const long long rows_all = static_cast<long long>(p.group) * T;
+  const int rows = tree_rows(rows_all);
+  p.row_tiles = static_cast<int>((rows_all + rows - 1) / rows);
+  p.box = 128;
+  while (page_size % p.box != 0) p.box /= 2;  // (page_size is a multiple of 16)
+  p.heads = static_cast<int*>(workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                       round256(kTreeMaxCtas * 4 * sizeof(int)));
+  p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   DeviceInfo di;
   st = current_device_info(&di);
   if (st != FA_OK) return st;
-  const cudaError_t e = launch_tree(d, dtype == FA_BF16, format == FA_CACHE_E4M3, p,
+  const long long most = static_cast<long long>(B) * Hk * p.row_tiles *
+                         ((static_cast<long long>(p.c.table_stride) * page_size + 127) / 128);
+  p.grid = di.num_sms < kTreeMaxCtas ? di.num_sms : kTreeMaxCtas;
+  if (most < p.grid) p.grid = static_cast<int>(most);
+  CUtensorMap tmk, tmv;
+  if (make_map_cache(&tmk, k_cache, p.c, d, p.box, format, dtype) != FA_OK ||
+      make_map_cache(&tmv, v_cache, p.c, d, p.box, format, dtype) != FA_OK)
+    return FA_ERR_CUDA;
+  const cudaError_t e = launch_tree(d, dtype == FA_BF16, format == FA_CACHE_E4M3, rows, tmk, tmv, p,
                                     static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -404,7 +404,8 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale
  *     and lse stay as they were.
  *   0 <= draft_lens[b] <= T and 0 <= ctx_lens[b] with ctx_lens[b] + n_b within
  *     the table are required; other values are clamped and reported.  With a
- *     bad page the results of its sequences are unspecified.
+ *     bad page the results of its sequences are unspecified.  A V scale below
+ *     2^-90 counts as 2^-90, one that is negative or infinite as NaN.
  *   workspace: fa_fwd_tree_workspace_size(B, Hq, Hk, T, d) bytes, 256-byte
  *     aligned; its contents on entry do not matter.  Calls that may overlap on
  *     the GPU need one each.

@@ -509,6 +509,26 @@ def test_tree_reports_bad_lengths_and_pages(fa):
         assert torch.equal(o[1], good[1])                   # the other sequence is right
 
 
+@pytest.mark.parametrize("e4m3,T", [(True, 3), (False, 3), (True, 70), (False, 70)])
+def test_tree_wait_timeout_is_reported_and_the_context_stays_usable(fa, e4m3, T):
+    """Ordinary waits, given 1 ns (as in test_gpu_timeout.py)."""
+    from exact_io_aware_47_b200 import _lib
+    c = Tree(B=3, Hq=4, Hk=2, T=T, ctx=(700, 0, 3000), d=128, page=16, dtype=BF16, e4m3=e4m3, seed=17)
+    good, _ = c.run(fa)
+    _ok(fa)
+    prev = _lib.fa_set_wait_limit_ns(1)
+    try:
+        c.run(fa)
+    finally:
+        _lib.fa_set_wait_limit_ns(prev)
+    st, word = fa.device_status()
+    assert st == _lib.FA_ERR_DEVICE_TIMEOUT, f"status {st} word {word:#x}"
+    assert (word >> 8) & 0xFF in range(61, 80), f"site of word {word:#x}"
+    again, _ = c.run(fa)
+    _ok(fa)
+    assert torch.equal(good, again)
+
+
 def test_tree_shared_pages_and_other_streams(fa):
     """Two sequences with the same prefix pages; a call on a side stream; two
     captured graphs that share one workspace, replayed in turn."""

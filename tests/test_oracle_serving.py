@@ -182,7 +182,7 @@ def _cache_cases(call):
     assert call(page=24) == U and call(page=8) == U
     assert call(pages=1 << 30, Hk=2) == U
     assert call(d=96) == U
-    assert call(kc=P + 8) == A and call(table=P + 2) == A and call(vs=P + 2) == A
+    assert call(kc=P + 8) == A and call(table=P + 2) == A and call(vs=P + 8) == A
 
 
 def test_cache_write_refusals(lib):
