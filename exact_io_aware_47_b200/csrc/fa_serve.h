@@ -77,7 +77,8 @@ struct TreeParams {
   int B, Hq, T, group;       // group = Hq / Hk
   float scale_log2;          // scale * log2(e)
   int row_tiles;             // ceil(group * T / rows of a tile)
-  int box;                   // keys of one TMA load: a power of two that divides page_size
+  int box, box_log2;         // keys of one TMA load: a power of two that divides page_size
+  unsigned page_mul, page_shift;  // x / page_size = umulhi(x, page_mul) >> page_shift, x < 2^31
   int grid;                  // CTAs
   int* heads;                // workspace: [grid][4], see fa_tree_kernel
   float* partial;            // workspace: [grid][2] slots

@@ -24,17 +24,25 @@
 // The scale of a K row multiplies its row of S^T, the scale of a V row its
 // row of P^T: both are one thread's.
 //
-// Softmax.  A thread owns one key and half of the R rows (columns of S^T).
-// Rows keep a reference exponent r (shared memory); probabilities are
-// 2^(z - r), their sums per thread and column stay in registers until the end
-// of the item.  r follows a row's maximum only when a score passes it by a
-// factor of 2^4 (2^8 for 16-bit P): the usual tile needs no maximum at all,
-// only one vote of the 128 threads that no score did.
+// Softmax.  A thread owns one key of a tile.  Rows keep a reference exponent r
+// (shared memory); probabilities are 2^(z - r), their sums per thread and
+// column stay in registers until the end of the item.  r follows a row's
+// maximum only when a score passes it by a factor of 2^4 (2^8 for 16-bit P):
+// the usual tile needs no maximum at all, only one vote of the 128 threads
+// that no score did.  Two groups of 128 threads work at it.  Up to 32 rows they
+// take turns, a tile each, with references, sums and an O of their own that
+// meet at the item's end (two chains of dependent steps run at once: what a
+// tile costs with few rows is latency); from 64 rows on they share each tile,
+// half of the columns each (a thread holds its columns in registers).
 //
-// Roles (384 threads, one CTA per SM): warps 0-3 and 4-7 softmax of the first
-// and second half of the columns, warp 8 loads (TMA), warp 9 issues MMAs, warps
-// 10-11 prepare Q.  The pipeline over tiles i is S(0) S(1) [PV(i) S(i+2)]...,
-// the loads come in the same order.
+// Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warps 8 and 9
+// load K and V (TMA), warp 12 the scales, warp 10 issues the products of S, warp
+// 11 those of O, warps 13-15 prepare Q.
+// An issuing thread pays about 60 cycles for an MMA and 210 for a commit
+// (measured, whatever the size), so S and O have a thread each, and there is
+// one commit per product: the barrier that gives a K or V slot back to the
+// loader is also what the softmax waits on for S and for finished products of O
+// (see TreeTiles).
 //
 // Work split.  All key tiles of all items form one line that is cut evenly
 // into one piece per CTA, whatever the lengths; an item that is cut leaves
@@ -44,14 +52,19 @@
 
 namespace fa {
 
-constexpr int kTreeThreads = 384;
-constexpr float kTreeNoRef = 1e30f;   // negated reference of a row without a key yet
+constexpr int kTreeThreads = 512;
+// Registers: 512 threads are launched with 128 each.  With 128 rows a softmax
+// thread holds 64 columns (scores and sums) and needs more: its warpgroups take
+// 184, the other two keep 72 (2 x 184 + 2 x 72 = 4 x 128).
+constexpr int kTreeLaunchRegs = 128, kTreeSoftmaxRegs = 184, kTreeOtherRegs = 72;
+static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, "register split");
 constexpr float kTreeMinScale = 0x1p-90f;  // V scales below count as this (keeps sums in range)
 
 template <int D_, bool BF16, bool E4M3, int R_>
 struct TreeLayout {
   static constexpr int D = D_, R = R_;
-  static constexpr int kCols = R / 2;                       // columns of a softmax thread
+  static constexpr bool kTurns = R <= 32;                   // the groups take turns at the tiles
+  static constexpr int kCols = kTurns ? R : R / 2;          // columns of a softmax thread
   static constexpr int kTermsQ = E4M3 ? (BF16 ? 2 : 3) : 1;
   static constexpr int kTermsP = E4M3 ? (BF16 ? 3 : 4) : 1;
   static constexpr int kPanels = (D * (E4M3 ? 1 : 2) + 127) / 128;  // 128-byte panels of a row
@@ -69,11 +82,15 @@ struct TreeLayout {
   static constexpr int kQBytes = kTermsQ * kPanels * kQPanel;
   static constexpr int kQBufs = R == 128 ? 1 : 2;
   static constexpr int kScales = E4M3 ? 8 : 0;              // ring of tile scales, 1 KB each
-  static constexpr int kStatBytes = (kQBufs + 3 + 4) * R * 4;
+  // per row: Q scales; per group and column: reference, its last change and
+  // factor, final weight; per softmax warp and column: one value
+  static constexpr int kStatBytes = (kQBufs * R + 2 * kCols * 4 + 8 * kCols + R) * 4;
   static constexpr int kFixed = kPBufs * kPBytes + kQBufs * kQBytes + kScales * 1024 + kStatBytes + 512 + 1024;
   static constexpr int kSlotsFit = (232448 - kFixed) / kSlotBytes;
   static constexpr int kSlots = kSlotsFit < 12 ? kSlotsFit : 12;
-  static_assert(kSlots >= 4, "K/V ring");
+  static constexpr int kSlotsK = kSlots / 2, kSlotsV = kSlots - kSlotsK;  // two rings
+  static_assert(kSlotsK >= 2, "a slot is reused two tiles later at the earliest (see below)");
+  static constexpr int kV = kSlotsK * kSlotBytes;
   static constexpr int kP = kSlots * kSlotBytes;
   static constexpr int kQ = kP + kPBufs * kPBytes;
   static constexpr int kScale = kQ + kQBufs * kQBytes;
@@ -81,7 +98,7 @@ struct TreeLayout {
   static constexpr int kBar = kStat + kStatBytes;
   static constexpr int kSmemBytes = kBar + 512 + 1024;      // + slack to align to 1024
   static constexpr int kOCols = kStack ? kTermsP * R : R;
-  static constexpr int kTmemUsed = 2 * R + kOCols;
+  static constexpr int kTmemUsed = 2 * R + (kTurns ? 2 : 1) * kOCols;
   static constexpr uint32_t kTmemCols = kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64
                                         : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
 };
@@ -141,10 +158,54 @@ __device__ __forceinline__ bool tree_next(TreeWalk& w, const TreeParams& p, Tree
   return true;
 }
 
-// Position in the load order K0 K1 V0 K2 V1 ... of the K and the V of tile i
-// of n.
-__device__ __forceinline__ int tree_k_pos(int i) { return i < 2 ? i : 2 * i - 1; }
-__device__ __forceinline__ int tree_v_pos(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
+// Tile i of a CTA uses slot i % n of the K and of the V ring (n slots) in round
+// i / n.  A slot's "empty" barrier ends a round's phase when the product that
+// reads the slot is complete: the loader waits for that, and so does the softmax:
+// in tile i for S(i), for O of tile i - 1 or i - 2, and at an item's end for O of
+// its last tile.  No phase can be missed there: with n >= 2 slots the next one
+// of the same slot belongs to S(i + 2), O(i) or a later tile, whose product
+// waits for that very softmax step (both issuing threads go in order).  Nor can
+// a wait be early (a parity wait returns at once while the phase before is still
+// open): whoever waits for a round of a slot has waited for the round before, or
+// for what followed from it.
+
+// The tiles of a CTA's piece in order, as the loading warps see them: where in
+// the cache this lane's keys (one TMA box of them) are.  Looked up a tile ahead
+// of its load; the page is only looked at then (place), so that the warp does
+// not wait for the table.
+struct TreePiece {
+  int page, hk, y;  // page, head and row in the page of the box
+  int count;        // boxes of the tile that hold keys of the sequence
+};
+struct TreeTiles {
+  TreeWalk walk;
+  TreeSeg seg;
+  int tile;
+  const int32_t* row;  // the sequence's row of the page table
+  __device__ __forceinline__ TreeTiles(const TreeWalk& w) : walk(w), seg{}, tile(0), row(nullptr) {}
+  __device__ __forceinline__ TreePiece next(const TreeParams& p, int lane, int pieces) {
+    if (tile == seg.t1) {
+      tree_next(walk, p, seg);
+      tile = seg.t0;
+      if (p.c.table) row = p.c.table + static_cast<long long>(seg.b) * p.c.table_stride;
+    }
+    const int left = seg.ctx + seg.drafts - tile * 128;   // keys from the tile's first on
+    TreePiece t{0, seg.hk, 0, min(pieces, (left + p.box - 1) >> p.box_log2)};
+    if (lane < t.count) {
+      const unsigned key = tile * 128 + lane * p.box;
+      const unsigned at = __umulhi(key, p.page_mul) >> p.page_shift;   // key / page_size
+      t.y = static_cast<int>(key - at * p.c.page_size);
+      t.page = seg.b;
+      if (row != nullptr) t.page = row[at];
+    }
+    ++tile;
+    return t;
+  }
+};
+// Slice (page and head) of a box; -1 if its page is not in the pool.
+__device__ __forceinline__ int tree_place(const TreeParams& p, const TreePiece& t) {
+  return t.page >= 0 && t.page < p.c.num_pages ? t.page * p.c.Hk + t.hk : -1;
+}
 
 // One MMA; operands by descriptor words (sdesc_lo, kSdescHi).
 template <bool E4M3>
@@ -204,10 +265,34 @@ __device__ __forceinline__ bool named_bar_or(int id, int threads, bool x) {
   return r != 0;
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
+// Maximum (which drops NaN) or sum over the warp's lanes of each of N columns,
+// to out[0 .. N).  Every exchange halves the columns that a lane still holds:
+// N - 1 shuffles (N <= 32) where one column at a time takes 5 N.
+template <int N, bool MAX>
+__device__ __forceinline__ void reduce_columns(float (&v)[N], int lane, float* out) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int step = 0; step < 5; ++step) {
+    const int o = 16 >> step;
+    const int held = N >> step;                  // columns before this exchange
+    if (held > 1) {
+      const bool hi = (lane & o) != 0;
+#pragma unroll
+      for (int j = 0; j < held / 2; ++j) {
+        const float send = hi ? v[j] : v[j + held / 2];
+        const float keep = hi ? v[j + held / 2] : v[j];
+        v[j] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
+      }
+    } else {
+      v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+  if constexpr (N >= 32) {
+#pragma unroll
+    for (int j = 0; j < N / 32; ++j) out[lane * (N / 32) + j] = v[j];
+  } else {
+    if (lane % (32 / N) == 0) out[lane / (32 / N)] = v[0];
+  }
 }
 
 // e4m3 bytes back to fp32 (two per call).
@@ -260,33 +345,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                    const TreeParams p) {
   using Lay = TreeLayout<D, BF16, E4M3, R>;
   constexpr int kCols = Lay::kCols;
-  constexpr int kSlots = Lay::kSlots;
+  constexpr int kSlots = Lay::kSlots, kSlotsK = Lay::kSlotsK, kSlotsV = Lay::kSlotsV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float* s_qs = reinterpret_cast<float*>(smem + Lay::kStat);  // [kQBufs][R] Q unscale x scale_log2
-  float* s_nr = s_qs + Lay::kQBufs * R;                       // [R] negated references
-  float* s_alpha = s_nr + R;                                  // [R]
-  float* s_sum = s_alpha + R;                                 // [R] 1 / sum, at the end
-  float* s_wmax = s_sum + R;                                  // [4][R] per-warp column values
+  float* s_nr = s_qs + Lay::kQBufs * R;                       // [2][kCols] negated references
+  float* s_move = s_nr + 2 * kCols;                           // [2][kCols] last change of s_nr
+  float* s_alpha = s_move + 2 * kCols;                        // [2][kCols] 2^s_move
+  float* s_weight = s_alpha + 2 * kCols;                      // [2][kCols] at the end: factor of O
+  float* s_warp = s_weight + 2 * kCols;                       // [8][kCols] per-warp column values
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
-  uint64_t* kv_full = bars;                     // [kSlots]
+  uint64_t* kv_full = bars;                     // [kSlots]: the K ring, the V ring
   uint64_t* kv_empty = kv_full + kSlots;        // [kSlots]
   uint64_t* sc_full = kv_empty + kSlots;        // [8]
   uint64_t* sc_empty = sc_full + 8;             // [8]
-  uint64_t* s_full = sc_empty + 8;              // [2]
-  uint64_t* p_full = s_full + 2;                // [2]
+  uint64_t* p_full = sc_empty + 8;              // [2]
   uint64_t* q_full = p_full + 2;                // [2]
   uint64_t* q_empty = q_full + 2;               // [2]
-  uint64_t* o_full = q_empty + 2;
-  uint64_t* pv_done = o_full + 1;
-  uint64_t* drain = pv_done + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = q_empty + 2;                // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_fix = abort_flag + 1;         // [2 parities][2 groups]
   TreeWalk* s_walk = reinterpret_cast<TreeWalk*>(const_cast<int*>(s_fix + 4));
-  long long* s_scan = reinterpret_cast<long long*>(smem + Lay::kStat);  // setup only [12 + 1]
-  static_assert(8 * (2 * 12 + 16 + 11) + 4 * 6 + sizeof(TreeWalk) <= 512, "barrier area");
-  static_assert(Lay::kStatBytes >= 13 * 8, "scan scratch");
+  long long* s_scan = reinterpret_cast<long long*>(smem + Lay::kStat);  // setup only, one per warp
+  static_assert(8 * (2 * 12 + 16 + 8) + 4 * 6 + sizeof(TreeWalk) <= 512, "barrier area");
+  static_assert(Lay::kStatBytes >= kTreeThreads / 32 * 8, "scan scratch");
   const WaitCtl wc{abort_flag, p.wait_ns};
 
   const int warp = threadIdx.x >> 5;
@@ -299,21 +382,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     for (int s = 0; s < 8; ++s) {
       mbar_init(&sc_full[s], 1);
-      mbar_init(&sc_empty[s], 8);
+      mbar_init(&sc_empty[s], Lay::kTurns ? 4 : 8);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 8);
-      mbar_init(&q_full[s], 2);
-      mbar_init(&q_empty[s], 9);
+      mbar_init(&p_full[s], Lay::kTurns ? 4 : 8);
+      mbar_init(&q_full[s], 3);
+      mbar_init(&q_empty[s], 8);
+      mbar_init(&drain[s], 1);
     }
-    mbar_init(o_full, 1);
-    mbar_init(pv_done, 1);
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 10) {
     tmem_alloc(tmem_slot, Lay::kTmemCols);
     tmem_relinquish();
   }
@@ -383,203 +463,200 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     head[3] = cont ? walk.drafts : 0;
   }
 
-  if (warp == 8) {
-    // ------------------------------------------------------------- loads
-    if (lane == 0) {
-      tma_prefetch_desc(&tmk);
-      tma_prefetch_desc(&tmv);
-    }
-    const int pieces = 128 / p.box;  // lane l < pieces loads keys l box .. of a tile
-    TreeSeg seg{};
-    bool more = tree_next(walk, p, seg);
-    int tile = seg.t0;
-    int z[2] = {0, 0}, y[2] = {0, 0};         // tiles i and i - 1
-    bool on[2] = {false, false};
-    int pos = 0, scales = 0;                  // slots, tile scales loaded
-    bool ok = true;
-    auto load_slot = [&](bool is_v, int zz, int yy, bool use) {
-      const int slot = pos % kSlots;
-      ok = mbar_wait_warp(&kv_empty[slot], ((pos / kSlots) & 1) ^ 1, wc, 61);
-      if (!ok) return;
-      const uint32_t mine = use ? static_cast<uint32_t>(Lay::kPanels * p.box * 128) : 0u;
-      const uint32_t all = __reduce_add_sync(0xffffffffu, mine);
-      if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], all);
+  if (warp >= 8) {
+  if constexpr (R == 128) regs_decrease<kTreeOtherRegs>();
+  if (warp == 8 || warp == 9) {
+    // ------------------------------------------------------------- K, V
+    const bool is_v = warp == 9;
+    const CUtensorMap* map = is_v ? &tmv : &tmk;
+    const int ring = is_v ? kSlotsV : kSlotsK;
+    uint64_t* full = kv_full + (is_v ? kSlotsK : 0);
+    uint64_t* empty = kv_empty + (is_v ? kSlotsK : 0);
+    uint8_t* slots = smem + (is_v ? Lay::kV : 0);
+    int slot = 0, round = 0;
+    if (lane == 0) tma_prefetch_desc(map);
+    const int pieces = 128 >> p.box_log2;  // lane l < pieces loads keys l box .. of a tile
+    TreeTiles at(walk);
+    TreePiece next{}, cur{};
+    if (n_tiles > 0) next = at.next(p, lane, pieces);
+    int loaded = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      cur = next;
+      if (i + 1 < n_tiles) next = at.next(p, lane, pieces);
+      if (!mbar_wait_warp(&empty[slot], (round & 1) ^ 1, wc, 61 + is_v)) break;
+      if (lane == 0)
+        mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(cur.count * p.box * 128 * Lay::kPanels));
       __syncwarp();
-      if (use) {
+      if (lane < cur.count) {
+        int z = tree_place(p, cur);
+        if (z < 0) {  // read as zeros, past the map's last slice
+          z = p.c.num_pages * p.c.Hk;
+          record_error(kErrDeviceSeqlen, 60);
+        }
 #pragma unroll
         for (int pn = 0; pn < Lay::kPanels; ++pn)
-          tma_load_3d(smem + slot * Lay::kSlotBytes + pn * 16384 + lane * p.box * 128,
-                      is_v ? &tmv : &tmk, &kv_full[slot], pn * Lay::kPanelElems, yy, zz);
+          tma_load_3d(slots + slot * Lay::kSlotBytes + pn * 16384 + lane * p.box * 128, map,
+                      &full[slot], pn * Lay::kPanelElems, cur.y, z);
       }
-      __syncwarp();
-      ++pos;
-    };
-    for (int i = 0; i <= n_tiles && ok; ++i) {
-      z[1] = z[0];
-      y[1] = y[0];
-      on[1] = on[0];
-      if (i < n_tiles && more) {
-        // K of tile i (and the scales of its rows)
-        const int L = seg.ctx + seg.drafts;
-        const int key = tile * 128 + lane * p.box;
-        on[0] = lane < pieces && key < L;
-        bool good = false;
-        if (on[0]) {
-          const int at = key / p.c.page_size;
-          const int page = p.c.table ? p.c.table[static_cast<long long>(seg.b) * p.c.table_stride + at] : seg.b;
-          good = page >= 0 && page < p.c.num_pages;
-          if (!good) record_error(kErrDeviceSeqlen, 62);
-          // (a page that is not in the pool: past the map's last slice, read as zeros)
-          z[0] = good ? page * p.c.Hk + seg.hk : p.c.num_pages * p.c.Hk;
-          y[0] = key - at * p.c.page_size;
-        }
-        load_slot(false, z[0], y[0], on[0]);
-        if (!ok) break;
-        if constexpr (E4M3) {
-          const int ss = i % Lay::kScales;
-          ok = mbar_wait_warp(&sc_empty[ss], ((i / Lay::kScales) & 1) ^ 1, wc, 63);
-          if (!ok) break;
-          const bool use = on[0] && good;
-          const uint32_t all = __reduce_add_sync(0xffffffffu, use ? 8u * p.box : 0u);
-          if (lane == 0) mbar_arrive_expect_tx(&sc_full[ss], all);
-          __syncwarp();
-          if (use) {
-            float* dst = reinterpret_cast<float*>(smem + Lay::kScale + ss * 1024) + lane * p.box;
-            const long long row = static_cast<long long>(z[0]) * p.c.page_size + y[0];
-            bulk_load(dst, p.c.k_scale + row, 4u * p.box, &sc_full[ss]);
-            bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &sc_full[ss]);
-          }
-          __syncwarp();
-          ++scales;
-        }
-        if (++tile == seg.t1) {
-          more = tree_next(walk, p, seg);
-          tile = seg.t0;
-        }
-      }
-      if (i >= 1) load_slot(true, z[1], y[1], on[1]);  // V(i - 1) follows K(i)
-    }
-    // never leave with copies in flight
-    for (int s = 0; s < kSlots; ++s) {
-      if (pos > s) {
-        const int last = pos - 1 - ((pos - 1 - s) % kSlots);
-        mbar_wait_drain(&kv_full[s], (last / kSlots) & 1, 200000000ull);
+      ++loaded;
+      if (++slot == ring) {
+        slot = 0;
+        ++round;
       }
     }
+    // never leave with copies in flight: the last load into every slot
+    for (int i = max(0, loaded - ring); i < loaded; ++i)
+      mbar_wait_drain(&full[i % ring], (i / ring) & 1, 200000000ull);
+    __syncwarp();
+  } else if (warp == 12) {
+    // ------------------------------------------------------------- scales
     if constexpr (E4M3) {
+      const int pieces = 128 >> p.box_log2;
+      TreeTiles at(walk);
+      TreePiece next{}, cur{};
+      if (n_tiles > 0) next = at.next(p, lane, pieces);
+      int done = 0;
+      for (int i = 0; i < n_tiles; ++i) {
+        cur = next;
+        if (i + 1 < n_tiles) next = at.next(p, lane, pieces);
+        const int ss = i % Lay::kScales;
+        if (!mbar_wait_warp(&sc_empty[ss], ((i / Lay::kScales) & 1) ^ 1, wc, 63)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sc_full[ss], 8u * p.box * cur.count);
+        __syncwarp();
+        if (lane < cur.count) {
+          float* dst = reinterpret_cast<float*>(smem + Lay::kScale + ss * 1024) + lane * p.box;
+          // (a bad page, reported by the K/V warp, takes the scales of page 0)
+          const long long slice = max(tree_place(p, cur), 0);
+          const long long row = slice * p.c.page_size + cur.y;
+          bulk_load(dst, p.c.k_scale + row, 4u * p.box, &sc_full[ss]);
+          bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &sc_full[ss]);
+        }
+        ++done;
+      }
       for (int s = 0; s < Lay::kScales; ++s) {
-        if (scales > s) {
-          const int last = scales - 1 - ((scales - 1 - s) % Lay::kScales);
+        if (done > s) {
+          const int last = done - 1 - ((done - 1 - s) % Lay::kScales);
           mbar_wait_drain(&sc_full[s], (last / Lay::kScales) & 1, 200000000ull);
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------- MMA issue
+  } else if (warp == 10) {
+    // ------------------------------------------------------------- S^T = K Q^T
     if (lane == 0 && n_tiles > 0) {
       constexpr uint32_t kFormat = E4M3 ? 0u : (BF16 ? 1u : 0u);
-      constexpr uint32_t kIdescS = (1u << 4) | (kFormat << 7) | (kFormat << 10) |
-                                   (static_cast<uint32_t>(R >> 3) << 17) | (8u << 24);
-      // A = V MN-major, B = P^T MN-major; e4m3 caches: B is e5m2 (format 1)
-      constexpr int kNPv = Lay::kOCols;
-      constexpr uint32_t kIdescO = (1u << 4) | (kFormat << 7) | ((E4M3 ? 1u : kFormat) << 10) |
-                                   (1u << 15) | (1u << 16) |
-                                   (static_cast<uint32_t>(kNPv >> 3) << 17) | (8u << 24);
+      constexpr uint32_t kIdesc = (1u << 4) | (kFormat << 7) | (kFormat << 10) |
+                                  (static_cast<uint32_t>(R >> 3) << 17) | (8u << 24);
       const uint32_t base = smem_addr(smem);
-      TreeWalk ws = walk, wo = walk;
-      TreeSeg ss{}, so{};
+      TreeSeg seg;
+      int i = 0;
       bool ok = true;
-      int s_tile = 0, s_segs = -1;  // tile of the segment of the next S, its index
-      auto issue_s = [&](int i) {
-        if (s_segs < 0 || s_tile == ss.t1) {
-          tree_next(ws, p, ss);
-          s_tile = ss.t0;
-          ++s_segs;
-          ok = mbar_wait(&q_full[s_segs % Lay::kQBufs], (s_segs / Lay::kQBufs) & 1, wc, 64);
-          if (!ok) return;
-        }
-        const int pos = tree_k_pos(i), slot = pos % kSlots;
-        ok = mbar_wait(&kv_full[slot], (pos / kSlots) & 1, wc, 65);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t a0 = sdesc_lo(base + slot * Lay::kSlotBytes, false);
-        const uint32_t b0 = sdesc_lo(base + Lay::kQ + (s_segs % Lay::kQBufs) * Lay::kQBytes, false);
-        const uint32_t d = tmem + (i & 1) * R;
+      for (int si = 0; ok && tree_next(walk, p, seg); ++si) {
+        const int qb = si % Lay::kQBufs;
+        ok = mbar_wait(&q_full[qb], (si / Lay::kQBufs) & 1, wc, 64);
+        const uint32_t b0 = sdesc_lo(base + Lay::kQ + qb * Lay::kQBytes, false);
+        for (int tile = seg.t0; ok && tile < seg.t1; ++tile, ++i) {
+          const int slot = i % kSlotsK;
+          // S(i - 2) has been read
+          if (i >= 2) ok = mbar_wait(&p_full[i & 1], ((i >> 1) - 1) & 1, wc, 65);
+          if (ok) ok = mbar_wait(&kv_full[slot], (i / kSlotsK) & 1, wc, 66);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a0 = sdesc_lo(base + slot * Lay::kSlotBytes, false);
+          const uint32_t d = tmem + (i & 1) * R;
 #pragma unroll
-        for (int t = 0; t < Lay::kTermsQ; ++t) {
+          for (int t = 0; t < Lay::kTermsQ; ++t) {
 #pragma unroll
-          for (int k = 0; k < Lay::kSteps; ++k)
-            tree_mma<E4M3>(d, a0 + (k >> 2) * 1024 + (k & 3) * 2,
-                           b0 + t * (Lay::kPanels * Lay::kQPanel >> 4) + (k >> 2) * (Lay::kQPanel >> 4) +
-                               (k & 3) * 2,
-                           kIdescS, t + k > 0);
+            for (int k = 0; k < Lay::kSteps; ++k)
+              tree_mma<E4M3>(d, a0 + (k >> 2) * 1024 + (k & 3) * 2,
+                             b0 + t * (Lay::kPanels * Lay::kQPanel >> 4) + (k >> 2) * (Lay::kQPanel >> 4) +
+                                 (k & 3) * 2,
+                             kIdesc, t + k > 0);
+          }
+          umma_commit(&kv_empty[slot]);
+          FA_TRACE_AT(i, 16);
         }
-        umma_commit(&s_full[i & 1]);
-        umma_commit(&kv_empty[slot]);
-        if (++s_tile == ss.t1) umma_commit(&q_empty[s_segs % Lay::kQBufs]);
-      };
-      int o_tile = 0;
-      bool o_begun = false;
-      auto issue_o = [&](int i) {
-        if (!o_begun || o_tile == so.t1) {
-          tree_next(wo, p, so);
-          o_tile = so.t0;
-          o_begun = true;
-        }
-        ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, wc, 66);
-        if (!ok) return;
-        const int pos = tree_v_pos(i, n_tiles), slot = pos % kSlots;
-        ok = mbar_wait(&kv_full[slot], (pos / kSlots) & 1, wc, 67);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t a0 = sdesc_lo(base + slot * Lay::kSlotBytes, true);
-        const uint32_t b0 = sdesc_lo(base + Lay::kP + (i % Lay::kPBufs) * Lay::kPBytes, true);
-        const uint32_t d = tmem + 2 * R;
-        constexpr int kKeySteps = E4M3 ? 4 : 8;                  // 32 or 16 keys each
-        constexpr uint32_t kKeyStep = E4M3 ? 256u : 128u;        // x 16 bytes
-        constexpr int kTerms = E4M3 && !Lay::kStack ? Lay::kTermsP : 1;
-        const bool first = o_tile == so.t0;
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) {
-#pragma unroll
-          for (int k = 0; k < kKeySteps; ++k)
-            tree_mma<E4M3>(d, a0 + k * kKeyStep, b0 + t * 1024 + k * kKeyStep, kIdescO,
-                           !first || t + k > 0);
-        }
-        umma_commit(&kv_empty[slot]);
-        umma_commit(pv_done);
-        if (++o_tile == so.t1) umma_commit(o_full);
-      };
-      issue_s(0);
-      if (ok && n_tiles > 1) issue_s(1);
-      for (int i = 0; i < n_tiles && ok; ++i) {
-        issue_o(i);
-        if (ok && i + 2 < n_tiles) issue_s(i + 2);
       }
-      umma_commit(drain);
-      mbar_wait_drain(drain, 0, 200000000ull);
+      umma_commit(&drain[0]);
+      mbar_wait_drain(&drain[0], 0, 200000000ull);
     }
     __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp == 11) {
+    // ------------------------------------------------------------- O^T += V^T P^T
+    if (lane == 0 && n_tiles > 0) {
+      // both operands MN-major; e4m3 caches: A is e4m3, B e5m2 (format 1)
+      constexpr uint32_t kFormat = E4M3 ? 0u : (BF16 ? 1u : 0u);
+      constexpr uint32_t kIdesc = (1u << 4) | (kFormat << 7) | ((E4M3 ? 1u : kFormat) << 10) |
+                                  (1u << 15) | (1u << 16) |
+                                  (static_cast<uint32_t>(Lay::kOCols >> 3) << 17) | (8u << 24);
+      constexpr int kKeySteps = E4M3 ? 4 : 8;                  // 32 or 16 keys each
+      constexpr uint32_t kKeyStep = E4M3 ? 256u : 128u;        // x 16 bytes
+      constexpr int kTerms = E4M3 && !Lay::kStack ? Lay::kTermsP : 1;
+      const uint32_t base = smem_addr(smem);
+      TreeSeg seg;
+      int i = 0;
+      bool ok = true;
+      while (ok && tree_next(walk, p, seg)) {
+        for (int tile = seg.t0; tile < seg.t1; ++tile, ++i) {
+          const int slot = i % kSlotsV;
+          ok = mbar_wait(&kv_full[kSlotsK + slot], (i / kSlotsV) & 1, wc, 67);
+          if (ok) ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, wc, 68);
+          if (!ok) break;
+          FA_TRACE_AT(i, 17);
+          tc_fence_after();
+          const uint32_t a0 = sdesc_lo(base + Lay::kV + slot * Lay::kSlotBytes, true);
+          const uint32_t b0 = sdesc_lo(base + Lay::kP + (i % Lay::kPBufs) * Lay::kPBytes, true);
+          const uint32_t d = tmem + 2 * R + (Lay::kTurns ? (i & 1) * Lay::kOCols : 0);
+          const bool first = tile - seg.t0 < (Lay::kTurns ? 2 : 1);
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) {
+#pragma unroll
+            for (int k = 0; k < kKeySteps; ++k)
+              tree_mma<E4M3>(d, a0 + k * kKeyStep, b0 + t * 1024 + k * kKeyStep, kIdesc,
+                             !first || t + k > 0);
+          }
+          umma_commit(&kv_empty[kSlotsK + slot]);
+          FA_TRACE_AT(i, 18);
+        }
+      }
+      umma_commit(&drain[1]);
+      mbar_wait_drain(&drain[1], 0, 200000000ull);
+    }
+    __syncwarp();
+  } else {
     // ------------------------------------------------------------- Q
     constexpr int kLanes = D / 8;                // lanes of a row, 8 values each
     constexpr int kRowsWarp = 32 / kLanes;
     const int rows_all = p.group * p.T;
+    constexpr int kIters = (R + 3 * kRowsWarp - 1) / (3 * kRowsWarp);  // of 3 warps x kRowsWarp rows
+    constexpr int kBatch = kIters < 8 ? kIters : 8;
+    const int sub = lane / kLanes, l = lane % kLanes;
     TreeSeg seg;
-    for (int si = 0; tree_next(walk, p, seg); ++si) {
+    bool ok = true;
+    for (int si = 0; ok && tree_next(walk, p, seg); ++si) {
       const int qb = si % Lay::kQBufs;
-      if (!mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 68)) break;
-      const int sub = lane / kLanes, l = lane % kLanes;
       const long long row0 = (static_cast<long long>(seg.b) * p.Hq + static_cast<long long>(seg.hk) * p.group) * p.T +
                              static_cast<long long>(seg.rt) * R;
       uint8_t* qdst = smem + Lay::kQ + qb * Lay::kQBytes;
-#pragma unroll 4
-      for (int r0 = (warp - 10) * kRowsWarp; r0 < R; r0 += 2 * kRowsWarp) {
-        const int r = r0 + sub;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (seg.rt * R + r < rows_all)
-          x = *(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D * 2) + l);
+#pragma unroll 1
+      for (int it0 = 0; it0 < kIters; it0 += kBatch) {
+        // a batch of loads in flight, the first one before the buffer is free
+        uint4 xs[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = ((it0 + k) * 3 + warp - 13) * kRowsWarp + sub;
+          xs[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < R && seg.rt * R + r < rows_all)
+            xs[k] = *(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D * 2) + l);
+        }
+        if (it0 == 0) {
+          ok = mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 69);
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+        const int r = ((it0 + k) * 3 + warp - 13) * kRowsWarp + sub;
+        const uint4 x = xs[k];
         if constexpr (E4M3) {
           float f[8];
           float amax = abs_max8(x, BF16, 0.f);
@@ -591,7 +668,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int e = amax > 0.f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23), 8), 253) : 134;
           const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
           const float down = __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
-          if (l == 0)
+          if (l == 0 && r < R)
             s_qs[qb * R + r] = amax < INFINITY ? down * p.scale_log2 : __int_as_float(0x7fffffff);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= up;
@@ -611,27 +688,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             // 8 bytes at column 8 l of row r: chunk l / 2, swizzled by the row
             const uint32_t at = r * 128 + ((((l >> 1) ^ (r & 7)) << 4) | ((l & 1) << 3));
-            *reinterpret_cast<uint2*>(qdst + t * Lay::kQPanel + at) = make_uint2(w[0], w[1]);
+            if (r < R) *reinterpret_cast<uint2*>(qdst + t * Lay::kQPanel + at) = make_uint2(w[0], w[1]);
           }
         } else {
           const uint32_t at = (l >> 3) * Lay::kQPanel + r * 128 + (((l & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(qdst + at) = x;
+          if (r < R) *reinterpret_cast<uint4*>(qdst + at) = x;
+        }
         }
       }
+      if (!ok) break;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
     }
     __syncwarp();
+  }
   } else {
+    if constexpr (R == 128) regs_increase<kTreeSoftmaxRegs>();
     // ------------------------------------------------------------- softmax
     const int grp = warp >> 2;
     const int tid = threadIdx.x & 127;           // key of the tile = TMEM lane; d at the end
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int col0 = grp * kCols;
+    const int col0 = Lay::kTurns ? 0 : grp * kCols;   // this thread's columns of S^T
     const int bar_id = 1 + grp;
-    float* nr = s_nr + col0;
-    float* alpha = s_alpha + col0;
+    float* nr = s_nr + grp * kCols;
+    float* move = s_move + grp * kCols;
+    float* alpha = s_alpha + grp * kCols;
+    const uint32_t tO = tmem + lane_off + 2 * R + (Lay::kTurns ? grp * Lay::kOCols : 0);
+    constexpr int kEvery = Lay::kTurns ? 2 : 1;       // tiles from one of this group to its next
     // a row's reference stands for P = 2^kBias, and moves when P would pass
     // 2^kOver.  e5m2 terms reach from 2^15 down to steps of 2^-16: the reference
     // at 2^11 leaves 2^4 above it and 2^-27 below; fp16 has steps of 2^-24.
@@ -640,23 +724,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int rows_all = p.group * p.T;
     bool ok = true;
     int i = 0;                                   // tile of this CTA
+    // S(i), O(i) complete (see TreeTiles)
+    auto wait_s = [&](int i, unsigned site) {
+      return mbar_wait_warp(&kv_empty[i % kSlotsK], (i / kSlotsK) & 1, wc, site);
+    };
+    auto wait_o = [&](int i, unsigned site) {
+      return mbar_wait_warp(&kv_empty[kSlotsK + i % kSlotsV], (i / kSlotsV) & 1, wc, site);
+    };
     TreeSeg seg;
     for (int si = 0; tree_next(walk, p, seg); ++si) {
       const int qb = si % Lay::kQBufs;
       const float* qs = s_qs + qb * R + col0;
       const int L = seg.ctx + seg.drafts;
       const int m0 = seg.rt * R + col0;          // first row of this thread's columns
-      const int t_first = m0 % p.T;
-      ok = mbar_wait_warp(&q_full[qb], (si / Lay::kQBufs) & 1, wc, 69) && ok;
-      if (tid < kCols) nr[tid] = kTreeNoRef;
+      ok = mbar_wait_warp(&q_full[qb], (si / Lay::kQBufs) & 1, wc, 70) && ok;
+      if (tid < kCols) nr[tid] = 0.f;
+      bool unset = true;                         // tid < kCols: column tid has no reference yet
       if (tid == 0) s_fix[(si & 1) * 2 + grp] = 0;
       // (a wait that gave up: this group goes on to the vote at the item's end)
       ok = named_bar_and(bar_id, 128, ok);
       const bool begun = ok;
+      bool force = true;                         // some column has no reference yet
       float sum[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) sum[c] = 0.f;
-      for (int tile = seg.t0; begun && tile < seg.t1; ++tile, ++i) {
+      const int i_end = i + seg.t1 - seg.t0;
+      // (turns: tile i of the CTA belongs to group i % 2)
+      int tile = seg.t0;
+      if (Lay::kTurns && (i & 1) != grp) {
+        ++tile;
+        ++i;
+      }
+      const bool any = tile < seg.t1;            // this group has a tile of the item
+      if (!any && lane == 0) mbar_arrive(&q_empty[qb]);
+      int last = i;                              // its last one
+      for (; begun && tile < seg.t1; tile += kEvery, i += kEvery) {
+        last = i;
         const int key = tile * 128 + tid;
         const int u = key - seg.ctx;             // drafted token, negative in the context
         // columns that see this key (only tiles with the end of the sequence
@@ -666,107 +769,145 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (edge && u >= 0) {
           seen = 0ull;
           if (u < seg.drafts) {
-            int t = t_first;
+            int t = m0 % p.T;
+            const uint8_t* column = p.mask ? p.mask + seg.b * p.mask_stride + u : nullptr;
+#pragma unroll 32
             for (int c = 0; c < kCols; ++c) {
-              if (tree_sees(p, seg.b, t, u)) seen |= 1ull << c;
+              const bool sees = column ? column[static_cast<long long>(t) * p.T] != 0 : u <= t;
+              seen |= static_cast<uint64_t>(sees) << c;
               if (++t == p.T) t = 0;
             }
           }
         }
-        float sk = 1.f, sv = 1.f;
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 0);
+        float sk = 1.f, sv = 1.f, lv = 0.f;
         if constexpr (E4M3) {
           const int ss = i % Lay::kScales;
-          ok = mbar_wait_warp(&sc_full[ss], (i / Lay::kScales) & 1, wc, 70) && ok;
+          ok = mbar_wait_warp(&sc_full[ss], (i / Lay::kScales) & 1, wc, 71) && ok;
           if (key < L) {
             const float* sc = reinterpret_cast<const float*>(smem + Lay::kScale + ss * 1024);
             sk = sc[tid];
             sv = sc[128 + tid];
-            // (a scale that is not a size makes its row's probabilities NaN)
             if (!(sv >= kTreeMinScale)) sv = sv >= 0.f ? kTreeMinScale : NAN;
             else if (sv == INFINITY) sv = NAN;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_empty[ss]);
+          lv = lg2_approx(sv);
         }
-        ok = mbar_wait_warp(&s_full[i & 1], (i >> 1) & 1, wc, 71) && ok;
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 1);
+        ok = wait_s(i, 72) && ok;  // S(i) is complete
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 2);
         tc_fence_after();
-        float x[kCols];
+        // d: exponent of a probability against its row's reference (without
+        // the V scale sv = 2^lv, which multiplies what is stored)
+        float d[kCols];
         {
           uint32_t raw[kCols];
           tmem_ld_cols<kCols>(tmem + lane_off + (i & 1) * R + col0, raw);
+          const unsigned long long f2 = E4M3 ? f2pack(sk, sk) : f2pack(p.scale_log2, p.scale_log2);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) x[c] = __uint_as_float(raw[c]) * (E4M3 ? sk : p.scale_log2);
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(nr + c);
+            unsigned long long a = f2pack(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1]));
+            unsigned long long b = f2pack(__uint_as_float(raw[c + 2]), __uint_as_float(raw[c + 3]));
+            if constexpr (E4M3) {
+              const float4 q4 = *reinterpret_cast<const float4*>(qs + c);
+              a = ffma2(fmul2(a, f2), f2pack(q4.x, q4.y), f2pack(n4.x, n4.y));
+              b = ffma2(fmul2(b, f2), f2pack(q4.z, q4.w), f2pack(n4.z, n4.w));
+            } else {
+              a = ffma2(a, f2, f2pack(n4.x, n4.y));
+              b = ffma2(b, f2, f2pack(n4.z, n4.w));
+            }
+            f2unpack(a, d[c], d[c + 1]);
+            f2unpack(b, d[c + 2], d[c + 3]);
+          }
         }
         if (edge && u >= 0) {
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
-            if (!((seen >> c) & 1)) x[c] = -INFINITY;
+            if (!((seen >> c) & 1)) d[c] = -INFINITY;
         }
-        // exponents against the references; z = x qs + log2 sv is the exponent
-        // of what is stored
-        const float lv = E4M3 ? log2f(sv) : 0.f;
-        const float limit = kOver - lv;
-        float top = -INFINITY;
+        if (E4M3 && !(sv == sv)) {
+          // a V row without a scale makes the rows that see it NaN, and no other
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const float dd = E4M3 ? fmaf(x[c], qs[c], nr[c]) : x[c] + nr[c];
-          top = fmaxf(top, dd);
+          for (int c = 0; c < kCols; ++c)
+            if ((seen >> c) & 1) d[c] = NAN;
+          sv = 0.f;
+          lv = 0.f;
         }
-        if (named_bar_or(bar_id, 128, top > limit || !ok)) {
+        float top = d[0];
+#pragma unroll
+        for (int c = 1; c + 1 < kCols; c += 2) top = fmax3(top, d[c], d[c + 1]);
+        top = fmaxf(top, d[kCols - 1]) + lv;
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 3);
+        if (named_bar_or(bar_id, 128, top > kOver || force || !ok)) {
           // some row's reference moves (or a wait gave up)
           if (!named_bar_and(bar_id, 128, ok)) { ok = false; break; }
+          {
+            float m[kCols];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            const float z = (E4M3 ? x[c] * qs[c] : x[c]) + lv;
-            const float m = warp_max(((seen >> c) & 1) ? z : -INFINITY);
-            if (lane == 0) s_wmax[(warp & 3) * R + col0 + c] = m;
+            for (int c = 0; c < kCols; ++c) m[c] = d[c] + lv;
+            reduce_columns<kCols, true>(m, lane, s_warp + warp * kCols);
           }
           named_bar_sync(bar_id, 128);
           if (tid < kCols) {
-            float m = s_wmax[col0 + tid];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) m = fmaxf(m, s_wmax[w * R + col0 + tid]);
-            const float old = nr[tid];
-            const float now = m > -INFINITY ? fminf(old, kBias - m) : old;
-            nr[tid] = now;
-            alpha[tid] = exp2f(now - old);  // 0 for a row that had no key yet
+            const float* w = s_warp + grp * 4 * kCols + tid;
+            const float m = fmaxf(fmaxf(w[0], w[kCols]), fmaxf(w[2 * kCols], w[3 * kCols]));
+            float by = 0.f, factor = 1.f;
+            if (m > -INFINITY && (unset || m > kBias)) {
+              by = kBias - m;
+              // (a row without a key so far has sums of zero)
+              if (!unset) factor = exp2f(by);
+              unset = false;
+            }
+            nr[tid] += by;
+            move[tid] = by;
+            alpha[tid] = factor;
           }
-          named_bar_sync(bar_id, 128);
+          force = named_bar_or(bar_id, 128, tid < kCols && unset);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) sum[c] *= alpha[c];
-          if (tile > seg.t0) {
-            // O^T: this thread is row d = tid.  Its products up to tile i - 2 are
-            // complete (S(i) was committed after them); PV(i - 1) is waited for.
-            ok = mbar_wait_warp(pv_done, (i - 1) & 1, wc, 72);
+          for (int c = 0; c < kCols; ++c) {
+            d[c] += move[c];
+            sum[c] *= alpha[c];
+          }
+          if (tile - seg.t0 >= kEvery) {
+            // O^T: this thread is row d = tid; the products so far have to be complete
+            ok = wait_o(i - kEvery, 73);
             if (!named_bar_and(bar_id, 128, ok)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
             for (int t = 0; t < Lay::kOCols / R; ++t) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < kCols; c += 8) {
-                const uint32_t at = tmem + lane_off + 2 * R + t * R + col0 + c;
+                const uint32_t at = tO + t * R + col0 + c;
                 uint32_t ro[8];
                 tmem_ld8(at, ro);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ro[e] = __float_as_uint(__uint_as_float(ro[e]) * alpha[c + e]);
+                for (int e = 0; e < 8; ++e)
+                  ro[e] = __float_as_uint(__uint_as_float(ro[e]) * alpha[c + e]);
                 tmem_st_n<8>(at, ro);
               }
             }
             tmem_st_wait();
           }
         }
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 4);
+        // the product that read this P buffer before is complete (so V(i - 2), and
+        // with it the slot's round before V(i)'s, is known to have come and gone)
+        if (i >= Lay::kPBufs) ok = wait_o(i - Lay::kPBufs, 75) && ok;
         // V rows that the cache does not hold are cleared (0 x NaN is NaN), and
         // drafted rows are searched for values that are not finite
         if (edge) {
-          const int pos = tree_v_pos(i, n_tiles), slot = pos % kSlots;
-          ok = mbar_wait_warp(&kv_full[slot], (pos / kSlots) & 1, wc, 73) && ok;
+          const int slot = i % kSlotsV;
+          ok = mbar_wait_warp(&kv_full[kSlotsK + slot], (i / kSlotsV) & 1, wc, 74) && ok;
           if (ok && u >= 0) {
-            uint8_t* row = smem + slot * Lay::kSlotBytes + tid * 128;
+            uint8_t* row = smem + Lay::kV + slot * Lay::kSlotBytes + tid * 128;
 #pragma unroll
             for (int pn = 0; pn < Lay::kPanels; ++pn) {
-#pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                uint4* at = reinterpret_cast<uint4*>(row + pn * 16384 + (grp * 4 + ch) * 16);
+#pragma unroll 4
+              for (int ch = Lay::kTurns ? 0 : grp * 4; ch < (Lay::kTurns ? 8 : grp * 4 + 4); ++ch) {
+                uint4* at = reinterpret_cast<uint4*>(row + pn * 16384 + ch * 16);
                 if (key >= L) {
                   *at = make_uint4(0u, 0u, 0u, 0u);
                 } else {
@@ -791,105 +932,134 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
           }
         }
-        if (Lay::kPBufs == 1 && i > 0)
-          ok = mbar_wait_warp(pv_done, (i - 1) & 1, wc, 74) && ok;
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 5);
         // probabilities, their sums, and P^T
         uint8_t* prow = smem + Lay::kP + (i % Lay::kPBufs) * Lay::kPBytes + tid * 128;
         const uint32_t swz = tid & 7;
-        if constexpr (E4M3) {
-          constexpr int kTerms = Lay::kTermsP;
+        constexpr int kStep = kCols < 16 ? 8 : 16;
+        const unsigned long long sv2 = f2pack(sv, sv);
 #pragma unroll
-          for (int c = 0; c < kCols; c += 8) {
-            uint32_t w[2][kTerms];
+        for (int c = 0; c < kCols; c += kStep) {
+          constexpr int kTerms = E4M3 ? Lay::kTermsP : 1;
+          uint32_t w[kTerms][kStep / 4];          // e5m2 terms, four columns a word
+          uint32_t h[kStep / 2];                  // 16-bit pairs
 #pragma unroll
-            for (int q4 = 0; q4 < 2; ++q4) {
-              float pr[4];
+          for (int e = 0; e < kStep; e += 4) {
+            float pr[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int cc = c + 4 * q4 + e;
-                const float ex = ex2_approx(fmaf(x[cc], qs[cc], nr[cc]));
-                sum[cc] += ex;
-                pr[e] = ((seen >> cc) & 1) ? ex * sv : 0.f;
-              }
-              e5m2_terms<kTerms>(pr[0], pr[1], pr[2], pr[3], w[q4]);
+            for (int o = 0; o < 4; o += 2) {
+              unsigned long long x = f2pack(ex2_approx(d[c + e + o]), ex2_approx(d[c + e + o + 1]));
+              const unsigned long long s2 = fadd2(f2pack(sum[c + e + o], sum[c + e + o + 1]), x);
+              f2unpack(s2, sum[c + e + o], sum[c + e + o + 1]);
+              if (E4M3) x = fmul2(x, sv2);
+              f2unpack(x, pr[o], pr[o + 1]);
             }
+            if constexpr (E4M3) {
+              uint32_t q[kTerms];
+              e5m2_terms<kTerms>(pr[0], pr[1], pr[2], pr[3], q);
+#pragma unroll
+              for (int t = 0; t < kTerms; ++t) w[t][e / 4] = q[t];
+            } else {
+              h[e / 2] = pack2<BF16>(pr[0], pr[1]);
+              h[e / 2 + 1] = pack2<BF16>(pr[2], pr[3]);
+            }
+          }
+          // kStep columns of the key's row of P^T, in 16-byte chunks swizzled by the row
+          auto chunk = [&](int byte) {
+            return prow + (byte >> 7) * 16384 + ((((byte >> 4) & 7) ^ swz) << 4) + (byte & 15);
+          };
+          if constexpr (E4M3) {
 #pragma unroll
             for (int t = 0; t < kTerms; ++t) {
-              const int at = t * R + col0 + c;   // byte of the key's row of P^T
-              *reinterpret_cast<uint2*>(prow + (at >> 7) * 16384 + ((((at >> 4) & 7) ^ swz) << 4) + (at & 8)) =
-                  make_uint2(w[0][t], w[1][t]);
+              uint8_t* to = chunk(t * R + col0 + c);
+              if constexpr (kStep == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[t][0], w[t][1]);
+              else *reinterpret_cast<uint4*>(to) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
             }
-          }
-        } else {
+          } else {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = ex2_approx(x[c + 2 * e] + nr[c + 2 * e]);
-              const float b = ex2_approx(x[c + 2 * e + 1] + nr[c + 2 * e + 1]);
-              sum[c + 2 * e] += a;
-              sum[c + 2 * e + 1] += b;
-              w[e] = pack2<BF16>(a, b);
-            }
-            const int at = 2 * (col0 + c);
-            *reinterpret_cast<uint4*>(prow + (at >> 7) * 16384 + ((((at >> 4) & 7) ^ swz) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < kStep / 2; e += 4)
+              *reinterpret_cast<uint4*>(chunk(2 * (col0 + c) + 4 * e)) =
+                  make_uint4(h[e], h[e + 1], h[e + 2], h[e + 3]);
           }
         }
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 6);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&p_full[i & 1]);
-          if (tile + 1 == seg.t1) mbar_arrive(&q_empty[qb]);
+          if (tile + kEvery >= seg.t1) mbar_arrive(&q_empty[qb]);
         }
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 7);
       }
       // ----------------------------------------------------------- end of the item
-      const bool whole = ok && mbar_wait_warp(o_full, si & 1, wc, 75);
+      const bool whole = ok && (!any || wait_o(last, 76));
+      i = i_end;
       if (!named_bar_and(3, 256, whole)) { ok = false; break; }
       tc_fence_after();
       // sums of the columns over the 128 keys' threads
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        float v = sum[c];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) s_wmax[(warp & 3) * R + col0 + c] = v;
-      }
-      named_bar_sync(bar_id, 128);
+      reduce_columns<kCols, false>(sum, lane, s_warp + warp * kCols);
+      named_bar_sync(3, 256);
       const bool complete = seg.t0 == 0 && seg.t1 == seg.nt;
       float* slot = p.partial + (2 * static_cast<size_t>(blockIdx.x) + (seg.t0 == 0 ? 1 : 0)) * tree_slot_floats<Lay>();
       const long long out0 = (static_cast<long long>(seg.b) * p.Hq + static_cast<long long>(seg.hk) * p.group) * p.T;
-      if (tid < kCols) {
-        float l = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) l += s_wmax[w * R + col0 + tid];
-        const int m = m0 + tid;
-        if (complete) {
-          s_sum[col0 + tid] = l == 0.f ? 0.f : 1.f / l;
-          if (m < rows_all && m % p.T < seg.drafts)
-            p.lse[out0 + m] = l == 0.f ? -INFINITY : (log2f(l) - nr[tid]) * 0.69314718055994531f;
+      // this group finishes columns e0 .. e0 + R / 2
+      const int e0 = grp * (R / 2);
+      if (tid < R / 2) {
+        const int col = e0 + tid, m = seg.rt * R + col;
+        auto total = [&](int g, int c) {
+          const float* w = s_warp + g * 4 * kCols + c;
+          return (w[0] + w[kCols]) + (w[2 * kCols] + w[3 * kCols]);
+        };
+        float l, top;                            // sum, reference
+        if constexpr (Lay::kTurns) {
+          const float l0 = total(0, col), l1 = total(1, col);
+          const float r0 = -s_nr[col], r1 = -s_nr[kCols + col];
+          top = fmaxf(l0 == 0.f ? -INFINITY : r0, l1 == 0.f ? -INFINITY : r1);
+          const float w0 = l0 == 0.f ? 0.f : exp2f(r0 - top), w1 = l1 == 0.f ? 0.f : exp2f(r1 - top);
+          l = (l0 == 0.f ? 0.f : w0 * l0) + (l1 == 0.f ? 0.f : w1 * l1);
+          const float inv = !complete ? 1.f : l == 0.f ? 0.f : 1.f / l;
+          s_weight[col] = w0 * inv;
+          s_weight[kCols + col] = w1 * inv;
         } else {
-          float2* st = reinterpret_cast<float2*>(slot + R * D) + col0 + tid;
-          *st = make_float2(-nr[tid], l);
+          l = total(grp, tid);
+          top = -nr[tid];
+          s_weight[grp * kCols + tid] = l == 0.f ? 0.f : complete ? 1.f / l : 1.f;
+        }
+        if (!complete) {
+          reinterpret_cast<float2*>(slot + R * D)[col] = make_float2(top, l);
+        } else if (m < rows_all && m % p.T < seg.drafts) {
+          p.lse[out0 + m] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
         }
       }
       named_bar_sync(bar_id, 128);
       const int fix = s_fix[(si & 1) * 2] | s_fix[(si & 1) * 2 + 1];
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 8) {
+      for (int c = 0; c < R / 2; c += 8) {
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 0.f;
 #pragma unroll
-        for (int t = 0; t < Lay::kOCols / R; ++t) {
-          uint32_t ro[8];
-          tmem_ld8(tmem + lane_off + 2 * R + t * R + col0 + c, ro);
+        for (int g = 0; g < (Lay::kTurns ? 2 : 1); ++g) {
+          float og[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] += __uint_as_float(ro[e]);
+          for (int e = 0; e < 8; ++e) og[e] = 0.f;
+#pragma unroll
+          for (int t = 0; t < Lay::kOCols / R; ++t) {
+            uint32_t ro[8];
+            tmem_ld8(tmem + lane_off + 2 * R + g * Lay::kOCols + t * R + e0 + c, ro);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) og[e] += __uint_as_float(ro[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            // (weight 0: no key seen, and maybe nothing written there)
+            const float w = Lay::kTurns ? s_weight[g * kCols + e0 + c + e] : s_weight[e0 + c + e];
+            o[e] += w == 0.f ? 0.f : w * og[e];
+          }
         }
         if (tid >= D) continue;                  // (d = 64: the upper lanes hold nothing)
+        const int m = seg.rt * R + e0 + c;       // first of 8 rows
         if (fix) {
           // drafted V rows with values that are not finite were cleared there:
           // add them for the queries that see them
@@ -901,81 +1071,123 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             else unpack2<BF16>(reinterpret_cast<const uint16_t*>(p.c.v)[row * D + tid], v, skip);
             if (fabsf(v) < INFINITY) continue;
             for (int e = 0; e < 8; ++e)
-              if (tree_sees(p, seg.b, (m0 + c + e) % p.T, key - seg.ctx)) o[e] += v;
+              if (tree_sees(p, seg.b, (m + e) % p.T, key - seg.ctx)) o[e] += v;
           }
         }
         if (complete) {
+          int t = m % p.T;
+          uint16_t* to = reinterpret_cast<uint16_t*>(p.o) + (out0 + m) * D + tid;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int m = m0 + c + e;
-            if (m < rows_all && m % p.T < seg.drafts) {
-              const float inv = s_sum[col0 + c + e];
-              const float y = inv == 0.f ? 0.f : o[e] * inv;
-              reinterpret_cast<uint16_t*>(p.o)[(out0 + m) * D + tid] =
-                  static_cast<uint16_t>(pack2<BF16>(y, 0.f));
-            }
+            if (m + e < rows_all && t < seg.drafts)
+              to[e * D] = static_cast<uint16_t>(pack2<BF16>(o[e], 0.f));
+            if (++t == p.T) t = 0;
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) slot[(col0 + c + e) * D + tid] = o[e];
+          for (int e = 0; e < 8; ++e) slot[(e0 + c + e) * D + tid] = o[e];
         }
       }
       tc_fence_before();
-      named_bar_sync(bar_id, 128);               // s_sum, s_wmax are reused
+      named_bar_sync(3, 256);                    // O and the statistics are reused
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tmem, Lay::kTmemCols);
   }
 }
 
-// Adds up the parts of the items that were cut.  Block (c, y): the item whose
-// first cut is at the start of CTA c's piece (if any), its rows y, y + gridDim.y
-// ...; a thread is a column of O.
+// Adds up the parts of the items that were cut, in the order of the keys.
+// Blocks (c, y): the item whose first cut is at the start of CTA c + 1's piece
+// (if any).  With ways = 1 a warp adds up a row (8 rows a block); with ways = 8 a
+// block does, each warp every 8th part.
+constexpr int kTreeJoinWarps = 8;
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(D) fa_tree_join_kernel(const TreeParams p, int R) {
+__global__ void __launch_bounds__(kTreeJoinWarps * 32) fa_tree_join_kernel(const TreeParams p, int R, int ways) {
+  constexpr int kVec = D / 32;                   // columns of a lane
+  constexpr int kRounds = kTreeMaxCtas / 32;     // parts of a lane
+  __shared__ float s_o[kTreeJoinWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x + 1;
-  const int* head = p.heads + c0 * 4;
-  const int b = head[0], item = head[1];
+  const int4* heads = reinterpret_cast<const int4*>(p.heads);
+  const int4 head = heads[c0];
+  const int b = head.x, item = head.y;
   if (b < 0) return;
   // (a CTA whose own first item is the same one did not begin it)
-  if (p.heads[(c0 - 1) * 4] == b && p.heads[(c0 - 1) * 4 + 1] == item) return;
-  int last = c0;
-  while (!p.heads[last * 4 + 2] && last + 1 < p.grid) ++last;
-  const size_t slot_floats = static_cast<size_t>(R) * (D + 2);
-  const float* first = p.partial + (2 * static_cast<size_t>(c0 - 1) + 1) * slot_floats;
-  const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
-  const long long out0 = (static_cast<long long>(b) * p.Hq + static_cast<long long>(hk) * p.group) * p.T;
-  const int drafts = head[3];
-  for (int r = blockIdx.y; r < R; r += gridDim.y) {
-    const int m = rt * R + r;
-    if (m >= p.group * p.T || m % p.T >= drafts) continue;
-    auto part = [&](int c) {
-      return c == c0 - 1 ? first : p.partial + 2 * static_cast<size_t>(c) * slot_floats;
-    };
-    float top = -INFINITY;
-    for (int c = c0 - 1; c <= last; ++c) {
-      const float2 st = reinterpret_cast<const float2*>(part(c) + R * D)[r];
-      if (st.y != 0.f) top = fmaxf(top, st.x);
-    }
-    float l = 0.f, o = 0.f;
-    for (int c = c0 - 1; c <= last; ++c) {
-      const float* s = part(c);
-      const float2 st = reinterpret_cast<const float2*>(s + R * D)[r];
-      const float w = st.y == 0.f ? 0.f : exp2f(st.x - top);
-      l += w * st.y;
-      o += w == 0.f ? 0.f : w * s[r * D + threadIdx.x];
-    }
-    const float y = l == 0.f ? 0.f : o / l;
-    reinterpret_cast<uint16_t*>(p.o)[(out0 + m) * D + threadIdx.x] =
-        static_cast<uint16_t>(pack2<BF16>(y, 0.f));
-    if (threadIdx.x == 0)
-      p.lse[out0 + m] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+  const int4 before = heads[c0 - 1];
+  if (before.x == b && before.y == item) return;
+  // parts: of CTA c0 - 1, which began the item, then of those that go on with it
+  int parts = 1;
+  for (int c = c0; c < p.grid; c += 32) {
+    int4 h = make_int4(-1, -1, 0, 0);
+    if (c + lane < p.grid) h = heads[c + lane];
+    const unsigned other = ~__ballot_sync(0xffffffffu, h.x == b && h.y == item);
+    parts += other ? __ffs(other) - 1 : 32;
+    if (other) break;
   }
+  const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
+  const int r = ways == 1 ? blockIdx.y * kTreeJoinWarps + warp : blockIdx.y;
+  const int m = rt * R + r;
+  if (r >= R || m >= p.group * p.T || m % p.T >= head.w) return;  // (ways = 8: the whole block)
+  const size_t slot_floats = static_cast<size_t>(R) * (D + 2);
+  auto part = [&](int i) {
+    return p.partial + (i == 0 ? 2 * static_cast<size_t>(c0 - 1) + 1 : 2 * static_cast<size_t>(c0 + i - 1)) * slot_floats;
+  };
+  // weight of a part: 2^(its reference - the largest); parts without a key: 0
+  float w[kRounds], ref[kRounds], l = 0.f, top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    float2 st = make_float2(0.f, 0.f);
+    if (k * 32 + lane < parts) st = reinterpret_cast<const float2*>(part(k * 32 + lane) + R * D)[r];
+    ref[k] = st.x;
+    w[k] = st.y;
+    if (st.y != 0.f) top = fmaxf(top, st.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const float sum = w[k];
+    w[k] = sum == 0.f ? 0.f : exp2f(ref[k] - top);
+    l += sum == 0.f ? 0.f : w[k] * sum;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float acc[kVec];
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+  const int way = ways == 1 ? 0 : warp;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+#pragma unroll 4
+    for (int j = way; j < 32; j += ways) {
+      if (k * 32 + j >= parts) break;
+      const float wi = __shfl_sync(0xffffffffu, w[k], j);
+      const float* from = part(k * 32 + j) + r * D + lane * kVec;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) acc[e] += wi == 0.f ? 0.f : wi * from[e];
+    }
+  }
+  if (ways > 1) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) s_o[warp][lane * kVec + e] = acc[e];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      for (int x = 1; x < kTreeJoinWarps; ++x) acc[e] += s_o[x][lane * kVec + e];
+  }
+  const long long row = (static_cast<long long>(b) * p.Hq + static_cast<long long>(hk) * p.group) * p.T + m;
+  uint32_t* to = reinterpret_cast<uint32_t*>(p.o) + (row * D + lane * kVec) / 2;
+#pragma unroll
+  for (int e = 0; e < kVec; e += 2)
+    to[e / 2] = pack2<BF16>(l == 0.f ? 0.f : acc[e] / l, l == 0.f ? 0.f : acc[e + 1] / l);
+  if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D, bool BF16, bool E4M3, int R>
@@ -983,12 +1195,26 @@ static cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                  cudaStream_t stream) {
   using Lay = TreeLayout<D, BF16, E4M3, R>;
   auto kern = fa_tree_kernel<D, BF16, E4M3, R>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
   if (e != cudaSuccess) return e;
+  if constexpr (R == 128) {
+    // the register split in the kernel assumes exactly this launch allocation
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kTreeLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   kern<<<p.grid, kTreeThreads, Lay::kSmemBytes, stream>>>(tmk, tmv, p);
   // items of one tile are never cut
   if (p.grid > 1 && static_cast<long long>(p.c.table_stride) * p.c.page_size > 128)
-    fa_tree_join_kernel<D, BF16><<<dim3(p.grid - 1, R < 16 ? R : 16), D, 0, stream>>>(p, R);
+  {
+    // few long items are cut into many parts: a block per row then
+    const int rows = std::min(R, p.group * p.T);
+    const long long items = static_cast<long long>(p.B) * p.c.Hk * p.row_tiles;
+    const int ways = items * kTreeJoinWarps <= p.grid ? kTreeJoinWarps : 1;
+    const unsigned ys = ways == 1 ? (rows + kTreeJoinWarps - 1) / kTreeJoinWarps : rows;
+    fa_tree_join_kernel<D, BF16><<<dim3(p.grid - 1, ys), kTreeJoinWarps * 32, 0, stream>>>(p, R, ways);
+  }
   return cudaGetLastError();
 }
 

@@ -419,6 +419,55 @@ def test_tree_lengths_differ_widely(fa, e4m3):
     assert torch.equal(o, o3) and torch.equal(lse, lse3)
 
 
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (FP16, 64), (FP16, 128)])
+@pytest.mark.parametrize("T", [1, 7, 13, 30])
+def test_tree_many_tiles_in_a_row(fa, dtype, d, e4m3, T):
+    """Enough keys that every SM works through tens of tiles and several items
+    (all rings go round many times), against float64 on the GPU."""
+    B, Hk, group, page = 14, 8, 4, 48
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    ctx = torch.randint(1, 7000, (B,), generator=g, device="cuda").to(torch.int32)
+    per = (7000 + T + page - 1) // page
+    table = torch.randperm(B * per, generator=g, device="cuda").view(B, per).to(torch.int32)
+    kc, vc, ks, vs = _pool(B * per, Hk, page, d, dtype, e4m3)
+    n = 7000 + T
+    k, v = (torch.randn(B, Hk, n, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    fa.cache_write(k, v, kc, vc, lens=ctx + T, block_table=table, k_scale=ks, v_scale=vs)
+    q = torch.randn(B, Hk * group, T, d, generator=g, device="cuda").to(dtype)
+    o, lse = fa.forward_tree(q, kc, vc, ctx, block_table=table, k_scale=ks, v_scale=vs)
+    _ok(fa)
+    half, scale = _half(dtype), d ** -0.5
+    causal = torch.ones(T, T, dtype=torch.bool, device="cuda").tril()
+    for b in range(B):
+        L = int(ctx[b]) + T
+        at = torch.arange(L, device="cuda")
+        pg, row = table[b].long()[at // page], at % page
+
+        def rows(c, s):
+            if not e4m3:
+                return c[pg, :, row].transpose(0, 1).double()
+            x = c.view(torch.uint8)[pg, :, row].view(torch.float8_e4m3fn).double()
+            return (x * s[pg, :, row].double().unsqueeze(-1)).transpose(0, 1)
+        kd, vd = rows(kc, ks), rows(vc, vs)                  # [Hk, L, d]
+        qd = q[b].double().view(Hk, group * T, d)
+        s = qd @ kd.transpose(1, 2) * scale
+        seen = torch.ones(T, L, dtype=torch.bool, device="cuda")
+        seen[:, L - T:] = causal
+        s = s.view(Hk, group, T, L).masked_fill(~seen, -math.inf).view(Hk, group * T, L)
+        rl = torch.logsumexp(s, -1)
+        pr = (s - rl.unsqueeze(-1)).exp()
+        ro, sp = pr @ vd, pr @ vd.abs()
+        ka = kd.abs().sum(-1).amax(-1)[:, None]
+        qk = (qd.abs() @ kd.abs().transpose(1, 2)).amax(-1)
+        e = scale * (2.0 ** -17 * qd.abs().amax(-1) * ka + 2 * d * 2.0 ** -24 * qk) + 2.0 ** -21
+        tol = half * ro.abs() + (half + 4 * e + L * 2.0 ** -23).unsqueeze(-1) * sp + 2.0 ** -25
+        err = (o[b].double().view(Hk, group * T, d) - ro).abs()
+        assert bool((err <= tol).all()), f"b{b} L{L}: worst {(err - tol).max().item():.3e}"
+        lerr = (lse[b].double().view(Hk, group * T) - rl).abs()
+        assert bool((lerr <= 2 * e + L * 2.0 ** -23 + 2.0 ** -22 * rl.abs()).all()), f"b{b}: LSE {lerr.max().item():.3e}"
+
+
 @pytest.mark.parametrize("dtype,e4m3", [(BF16, True), (FP16, True), (BF16, False)])
 def test_tree_one_key_takes_most_of_the_weight(fa, dtype, e4m3):
     """A first key with scores far above the others', whose sum still counts:
