@@ -42,7 +42,7 @@
 // (measured, whatever the size), so S and O have a thread each, and there is
 // one commit per product: the barrier that gives a K or V slot back to the
 // loader is also what the softmax waits on for S and for finished products of O
-// (see TreeTiles).
+// (see below, at the rings).
 //
 // Work split.  All key tiles of all items form one line that is cut evenly
 // into one piece per CTA, whatever the lengths; an item that is cut leaves
@@ -75,6 +75,8 @@ struct TreeLayout {
   // columns, summed at the end); with 128 rows each has its own panel and its
   // own product into the same columns
   static constexpr bool kStack = E4M3 && R < 128;
+  static constexpr bool kStackQ = kTurns && kTermsQ > 1;    // the terms of Q likewise
+  static constexpr int kSCols = kStackQ ? kTermsQ * R : R;
   static constexpr int kPRow = E4M3 ? kTermsP * R : 2 * R;  // bytes of a key's row of P^T
   static constexpr int kPBytes = (kPRow + 127) / 128 * 16384;
   static constexpr int kPBufs = R == 128 ? 1 : 2;
@@ -98,7 +100,9 @@ struct TreeLayout {
   static constexpr int kBar = kStat + kStatBytes;
   static constexpr int kSmemBytes = kBar + 512 + 1024;      // + slack to align to 1024
   static constexpr int kOCols = kStack ? kTermsP * R : R;
-  static constexpr int kTmemUsed = 2 * R + (kTurns ? 2 : 1) * kOCols;
+  static constexpr int kTmemO = 2 * kSCols;                 // S twice, then O
+  static constexpr int kTmemUsed = kTmemO + (kTurns ? 2 : 1) * kOCols;
+  static_assert(kTmemUsed <= 512, "TMEM columns");
   static constexpr uint32_t kTmemCols = kTmemUsed <= 32 ? 32 : kTmemUsed <= 64 ? 64
                                         : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
 };
@@ -125,8 +129,8 @@ __device__ __forceinline__ int tree_tiles(const TreeLens& l) {
 
 // This CTA's walk over its piece of the line of key tiles, item by item.
 struct TreeWalk {
-  int b, item, tile, nt;  // next item of sequence b (nt tiles each), first tile in it
-  int left;               // tiles left in the piece
+  int b, hk, rt, tile, nt;  // next item of sequence b (nt tiles each), first tile in it
+  int left;                 // tiles left in the piece
   int ctx, drafts;
 };
 struct TreeSeg {
@@ -136,17 +140,16 @@ struct TreeSeg {
 };
 __device__ __forceinline__ bool tree_next(TreeWalk& w, const TreeParams& p, TreeSeg& s) {
   if (w.left <= 0) return false;
-  const int items = p.c.Hk * p.row_tiles;
-  while (w.item >= items || w.nt == 0) {
+  while (w.hk >= p.c.Hk || w.nt == 0) {
     const TreeLens l = tree_lens(p, ++w.b);
     w.nt = tree_tiles(l);
     w.ctx = l.ctx;
     w.drafts = l.drafts;
-    w.item = 0;
+    w.hk = w.rt = 0;
   }
   s.b = w.b;
-  s.hk = w.item / p.row_tiles;
-  s.rt = w.item - s.hk * p.row_tiles;
+  s.hk = w.hk;
+  s.rt = w.rt;
   s.t0 = w.tile;
   s.t1 = min(w.nt, w.tile + w.left);
   s.nt = w.nt;
@@ -154,11 +157,14 @@ __device__ __forceinline__ bool tree_next(TreeWalk& w, const TreeParams& p, Tree
   s.drafts = w.drafts;
   w.left -= s.t1 - s.t0;
   w.tile = 0;
-  ++w.item;
+  if (++w.rt == p.row_tiles) {
+    w.rt = 0;
+    ++w.hk;
+  }
   return true;
 }
 
-// Tile i of a CTA uses slot i % n of the K and of the V ring (n slots) in round
+// Rings.  Tile i of a CTA uses slot i % n of the K and of the V ring (n slots) in round
 // i / n.  A slot's "empty" barrier ends a round's phase when the product that
 // reads the slot is complete: the loader waits for that, and so does the softmax:
 // in tile i for S(i), for O of tile i - 1 or i - 2, and at an item's end for O of
@@ -169,42 +175,53 @@ __device__ __forceinline__ bool tree_next(TreeWalk& w, const TreeParams& p, Tree
 // open): whoever waits for a round of a slot has waited for the round before, or
 // for what followed from it.
 
-// The tiles of a CTA's piece in order, as the loading warps see them: where in
-// the cache this lane's keys (one TMA box of them) are.  Looked up a tile ahead
-// of its load; the page is only looked at then (place), so that the warp does
-// not wait for the table.
-struct TreePiece {
-  int page, hk, y;  // page, head and row in the page of the box
-  int count;        // boxes of the tile that hold keys of the sequence
+// The tiles of a CTA's piece in order, as the loading warps see them.  A tile
+// takes 128 / box copies (one page may hold less than a tile); a warp looks up
+// the places of 32 copies at once, i.e. of several tiles of an item, and the
+// next batch's before it issues this one's, so that no copy waits for the page
+// table.
+struct TreeBatch {
+  int tiles;        // tiles of the batch (0: none left)
+  int left;         // keys of the sequence from the batch's first tile on
+  int page, hk, y;  // this lane's copy: page, head, row in the page
 };
 struct TreeTiles {
   TreeWalk walk;
   TreeSeg seg;
   int tile;
-  const int32_t* row;  // the sequence's row of the page table
-  __device__ __forceinline__ TreeTiles(const TreeWalk& w) : walk(w), seg{}, tile(0), row(nullptr) {}
-  __device__ __forceinline__ TreePiece next(const TreeParams& p, int lane, int pieces) {
+  __device__ __forceinline__ TreeTiles(const TreeWalk& w) : walk(w), seg{}, tile(0) {}
+  __device__ __forceinline__ TreeBatch next(const TreeParams& p, int lane) {
+    TreeBatch b{0, 0, 0, 0, 0};
     if (tile == seg.t1) {
-      tree_next(walk, p, seg);
+      if (!tree_next(walk, p, seg)) return b;
       tile = seg.t0;
-      if (p.c.table) row = p.c.table + static_cast<long long>(seg.b) * p.c.table_stride;
     }
-    const int left = seg.ctx + seg.drafts - tile * 128;   // keys from the tile's first on
-    TreePiece t{0, seg.hk, 0, min(pieces, (left + p.box - 1) >> p.box_log2)};
-    if (lane < t.count) {
-      const unsigned key = tile * 128 + lane * p.box;
+    const int per = 7 - p.box_log2;              // log2 of the copies of a tile
+    b.tiles = min(32 >> per, seg.t1 - tile);
+    b.left = seg.ctx + seg.drafts - tile * 128;
+    b.hk = seg.hk;
+    const int off = (lane >> per) * 128 + (lane & ((1 << per) - 1)) * p.box;
+    if (off < min(b.left, b.tiles * 128)) {
+      const unsigned key = tile * 128 + off;
       const unsigned at = __umulhi(key, p.page_mul) >> p.page_shift;   // key / page_size
-      t.y = static_cast<int>(key - at * p.c.page_size);
-      t.page = seg.b;
-      if (row != nullptr) t.page = row[at];
+      b.y = static_cast<int>(key - at * p.c.page_size);
+      b.page = p.c.table ? p.c.table[static_cast<long long>(seg.b) * p.c.table_stride + at] : seg.b;
     }
-    ++tile;
-    return t;
+    tile += b.tiles;
+    return b;
+  }
+  // Copies of tile j of a batch; this lane does one if it is its turn.
+  static __device__ __forceinline__ int copies(const TreeParams& p, const TreeBatch& b, int j) {
+    return min(128, b.left - j * 128 + p.box - 1) >> p.box_log2;
+  }
+  static __device__ __forceinline__ int turn(const TreeParams& p, int j, int lane) {
+    const int per = 7 - p.box_log2;
+    return (lane >> per) == j ? lane & ((1 << per) - 1) : 128;
   }
 };
-// Slice (page and head) of a box; -1 if its page is not in the pool.
-__device__ __forceinline__ int tree_place(const TreeParams& p, const TreePiece& t) {
-  return t.page >= 0 && t.page < p.c.num_pages ? t.page * p.c.Hk + t.hk : -1;
+// Slice (page and head) of a copy; -1 if its page is not in the pool.
+__device__ __forceinline__ int tree_place(const TreeParams& p, const TreeBatch& b) {
+  return b.page >= 0 && b.page < p.c.num_pages ? b.page * p.c.Hk + b.hk : -1;
 }
 
 // One MMA; operands by descriptor words (sdesc_lo, kSdescHi).
@@ -434,7 +451,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const long long here = static_cast<long long>(nt) * items;
         if (p0 < at + here) {
           s_walk->b = b;
-          s_walk->item = static_cast<int>((p0 - at) / nt);
+          const int item = static_cast<int>((p0 - at) / nt);
+          s_walk->hk = item / p.row_tiles;
+          s_walk->rt = item % p.row_tiles;
           s_walk->tile = static_cast<int>((p0 - at) % nt);
           s_walk->nt = nt;
           s_walk->left = static_cast<int>(p1 - p0);
@@ -458,7 +477,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     int* head = p.heads + blockIdx.x * 4;
     const bool cont = n_tiles > 0 && walk.tile > 0;
     head[0] = cont ? walk.b : -1;
-    head[1] = cont ? walk.item : -1;
+    head[1] = cont ? walk.hk * p.row_tiles + walk.rt : -1;
     head[2] = cont && walk.tile + n_tiles >= walk.nt;  // it ends here
     head[3] = cont ? walk.drafts : 0;
   }
@@ -475,33 +494,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     uint8_t* slots = smem + (is_v ? Lay::kV : 0);
     int slot = 0, round = 0;
     if (lane == 0) tma_prefetch_desc(map);
-    const int pieces = 128 >> p.box_log2;  // lane l < pieces loads keys l box .. of a tile
     TreeTiles at(walk);
-    TreePiece next{}, cur{};
-    if (n_tiles > 0) next = at.next(p, lane, pieces);
+    TreeBatch next = at.next(p, lane);
     int loaded = 0;
-    for (int i = 0; i < n_tiles; ++i) {
-      cur = next;
-      if (i + 1 < n_tiles) next = at.next(p, lane, pieces);
-      if (!mbar_wait_warp(&empty[slot], (round & 1) ^ 1, wc, 61 + is_v)) break;
-      if (lane == 0)
-        mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(cur.count * p.box * 128 * Lay::kPanels));
-      __syncwarp();
-      if (lane < cur.count) {
-        int z = tree_place(p, cur);
-        if (z < 0) {  // read as zeros, past the map's last slice
-          z = p.c.num_pages * p.c.Hk;
-          record_error(kErrDeviceSeqlen, 60);
-        }
-#pragma unroll
-        for (int pn = 0; pn < Lay::kPanels; ++pn)
-          tma_load_3d(slots + slot * Lay::kSlotBytes + pn * 16384 + lane * p.box * 128, map,
-                      &full[slot], pn * Lay::kPanelElems, cur.y, z);
+    bool ok = true;
+    while (ok && next.tiles > 0) {
+      const TreeBatch cur = next;
+      next = at.next(p, lane);
+      int z = tree_place(p, cur);
+      if (z < 0) {  // read as zeros, past the map's last slice
+        z = p.c.num_pages * p.c.Hk;
+        record_error(kErrDeviceSeqlen, 60);
       }
-      ++loaded;
-      if (++slot == ring) {
-        slot = 0;
-        ++round;
+      for (int j = 0; j < cur.tiles; ++j) {
+        ok = mbar_wait_warp(&empty[slot], (round & 1) ^ 1, wc, 61 + is_v);
+        if (!ok) break;
+        const int copies = TreeTiles::copies(p, cur, j), mine = TreeTiles::turn(p, j, lane);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(copies * p.box * 128 * Lay::kPanels));
+        __syncwarp();
+        if (mine < copies) {
+#pragma unroll
+          for (int pn = 0; pn < Lay::kPanels; ++pn)
+            tma_load_3d(slots + slot * Lay::kSlotBytes + pn * 16384 + mine * p.box * 128, map,
+                        &full[slot], pn * Lay::kPanelElems, cur.y, z);
+        }
+        ++loaded;
+        if (++slot == ring) {
+          slot = 0;
+          ++round;
+        }
       }
     }
     // never leave with copies in flight: the last load into every slot
@@ -511,27 +533,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   } else if (warp == 12) {
     // ------------------------------------------------------------- scales
     if constexpr (E4M3) {
-      const int pieces = 128 >> p.box_log2;
       TreeTiles at(walk);
-      TreePiece next{}, cur{};
-      if (n_tiles > 0) next = at.next(p, lane, pieces);
+      TreeBatch next = at.next(p, lane);
       int done = 0;
-      for (int i = 0; i < n_tiles; ++i) {
-        cur = next;
-        if (i + 1 < n_tiles) next = at.next(p, lane, pieces);
-        const int ss = i % Lay::kScales;
-        if (!mbar_wait_warp(&sc_empty[ss], ((i / Lay::kScales) & 1) ^ 1, wc, 63)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sc_full[ss], 8u * p.box * cur.count);
-        __syncwarp();
-        if (lane < cur.count) {
-          float* dst = reinterpret_cast<float*>(smem + Lay::kScale + ss * 1024) + lane * p.box;
-          // (a bad page, reported by the K/V warp, takes the scales of page 0)
-          const long long slice = max(tree_place(p, cur), 0);
-          const long long row = slice * p.c.page_size + cur.y;
-          bulk_load(dst, p.c.k_scale + row, 4u * p.box, &sc_full[ss]);
-          bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &sc_full[ss]);
+      bool ok = true;
+      while (ok && next.tiles > 0) {
+        const TreeBatch cur = next;
+        next = at.next(p, lane);
+        // (a bad page, reported by the K and V warps, takes the scales of page 0)
+        const long long row = static_cast<long long>(max(tree_place(p, cur), 0)) * p.c.page_size + cur.y;
+        for (int j = 0; j < cur.tiles; ++j) {
+          const int ss = done % Lay::kScales;
+          ok = mbar_wait_warp(&sc_empty[ss], ((done / Lay::kScales) & 1) ^ 1, wc, 63);
+          if (!ok) break;
+          const int copies = TreeTiles::copies(p, cur, j), mine = TreeTiles::turn(p, j, lane);
+          if (lane == 0) mbar_arrive_expect_tx(&sc_full[ss], 8u * p.box * copies);
+          __syncwarp();
+          if (mine < copies) {
+            float* dst = reinterpret_cast<float*>(smem + Lay::kScale + ss * 1024) + mine * p.box;
+            bulk_load(dst, p.c.k_scale + row, 4u * p.box, &sc_full[ss]);
+            bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &sc_full[ss]);
+          }
+          ++done;
         }
-        ++done;
       }
       for (int s = 0; s < Lay::kScales; ++s) {
         if (done > s) {
@@ -546,26 +570,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (lane == 0 && n_tiles > 0) {
       constexpr uint32_t kFormat = E4M3 ? 0u : (BF16 ? 1u : 0u);
       constexpr uint32_t kIdesc = (1u << 4) | (kFormat << 7) | (kFormat << 10) |
-                                  (static_cast<uint32_t>(R >> 3) << 17) | (8u << 24);
+                                  (static_cast<uint32_t>(Lay::kSCols >> 3) << 17) | (8u << 24);
+      constexpr int kPasses = Lay::kStackQ ? 1 : Lay::kTermsQ;
       const uint32_t base = smem_addr(smem);
       TreeSeg seg;
-      int i = 0;
+      int i = 0, slot = 0, round = 0;
       bool ok = true;
       for (int si = 0; ok && tree_next(walk, p, seg); ++si) {
         const int qb = si % Lay::kQBufs;
         ok = mbar_wait(&q_full[qb], (si / Lay::kQBufs) & 1, wc, 64);
         const uint32_t b0 = sdesc_lo(base + Lay::kQ + qb * Lay::kQBytes, false);
         for (int tile = seg.t0; ok && tile < seg.t1; ++tile, ++i) {
-          const int slot = i % kSlotsK;
           // S(i - 2) has been read
           if (i >= 2) ok = mbar_wait(&p_full[i & 1], ((i >> 1) - 1) & 1, wc, 65);
-          if (ok) ok = mbar_wait(&kv_full[slot], (i / kSlotsK) & 1, wc, 66);
+          // With many rows the products take long, and O(i - 2) is what the softmax
+          // waits for next: let it finish first, S(i) has time.
+          if (!Lay::kTurns && ok && i >= 2)
+            ok = mbar_wait(&kv_empty[kSlotsK + (i - 2) % kSlotsV], ((i - 2) / kSlotsV) & 1, wc, 77);
+          if (ok) ok = mbar_wait(&kv_full[slot], round & 1, wc, 66);
           if (!ok) break;
           tc_fence_after();
           const uint32_t a0 = sdesc_lo(base + slot * Lay::kSlotBytes, false);
-          const uint32_t d = tmem + (i & 1) * R;
+          const uint32_t d = tmem + (i & 1) * Lay::kSCols;
 #pragma unroll
-          for (int t = 0; t < Lay::kTermsQ; ++t) {
+          for (int t = 0; t < kPasses; ++t) {
 #pragma unroll
             for (int k = 0; k < Lay::kSteps; ++k)
               tree_mma<E4M3>(d, a0 + (k >> 2) * 1024 + (k & 3) * 2,
@@ -574,6 +602,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                              kIdesc, t + k > 0);
           }
           umma_commit(&kv_empty[slot]);
+          if (++slot == kSlotsK) {
+            slot = 0;
+            ++round;
+          }
           FA_TRACE_AT(i, 16);
         }
       }
@@ -594,19 +626,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       constexpr int kTerms = E4M3 && !Lay::kStack ? Lay::kTermsP : 1;
       const uint32_t base = smem_addr(smem);
       TreeSeg seg;
-      int i = 0;
+      int i = 0, slot = 0, round = 0;
       bool ok = true;
       while (ok && tree_next(walk, p, seg)) {
         for (int tile = seg.t0; tile < seg.t1; ++tile, ++i) {
-          const int slot = i % kSlotsV;
-          ok = mbar_wait(&kv_full[kSlotsK + slot], (i / kSlotsV) & 1, wc, 67);
+          ok = mbar_wait(&kv_full[kSlotsK + slot], round & 1, wc, 67);
           if (ok) ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, wc, 68);
           if (!ok) break;
           FA_TRACE_AT(i, 17);
           tc_fence_after();
           const uint32_t a0 = sdesc_lo(base + Lay::kV + slot * Lay::kSlotBytes, true);
           const uint32_t b0 = sdesc_lo(base + Lay::kP + (i % Lay::kPBufs) * Lay::kPBytes, true);
-          const uint32_t d = tmem + 2 * R + (Lay::kTurns ? (i & 1) * Lay::kOCols : 0);
+          const uint32_t d = tmem + Lay::kTmemO + (Lay::kTurns ? (i & 1) * Lay::kOCols : 0);
           const bool first = tile - seg.t0 < (Lay::kTurns ? 2 : 1);
 #pragma unroll
           for (int t = 0; t < kTerms; ++t) {
@@ -616,6 +647,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                              !first || t + k > 0);
           }
           umma_commit(&kv_empty[kSlotsK + slot]);
+          if (++slot == kSlotsV) {
+            slot = 0;
+            ++round;
+          }
           FA_TRACE_AT(i, 18);
         }
       }
@@ -714,7 +749,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     float* nr = s_nr + grp * kCols;
     float* move = s_move + grp * kCols;
     float* alpha = s_alpha + grp * kCols;
-    const uint32_t tO = tmem + lane_off + 2 * R + (Lay::kTurns ? grp * Lay::kOCols : 0);
+    const uint32_t tO = tmem + lane_off + Lay::kTmemO + (Lay::kTurns ? grp * Lay::kOCols : 0);
     constexpr int kEvery = Lay::kTurns ? 2 : 1;       // tiles from one of this group to its next
     // a row's reference stands for P = 2^kBias, and moves when P would pass
     // 2^kOver.  e5m2 terms reach from 2^15 down to steps of 2^-16: the reference
@@ -724,12 +759,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int rows_all = p.group * p.T;
     bool ok = true;
     int i = 0;                                   // tile of this CTA
-    // S(i), O(i) complete (see TreeTiles)
+    // S(i), O(i) complete
     auto wait_s = [&](int i, unsigned site) {
       return mbar_wait_warp(&kv_empty[i % kSlotsK], (i / kSlotsK) & 1, wc, site);
     };
     auto wait_o = [&](int i, unsigned site) {
       return mbar_wait_warp(&kv_empty[kSlotsK + i % kSlotsV], (i / kSlotsV) & 1, wc, site);
+    };
+    // scales of this thread's row in tile i, taken from the ring while the tile
+    // before is worked at
+    float sk = 1.f, sv = 1.f;
+    auto take_scales = [&](int i) {
+      const int ss = i % Lay::kScales;
+      const bool ready = mbar_wait_warp(&sc_full[ss], (i / Lay::kScales) & 1, wc, 71);
+      const float* sc = reinterpret_cast<const float*>(smem + Lay::kScale + ss * 1024);
+      sk = sc[tid];
+      sv = sc[128 + tid];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc_empty[ss]);
+      return ready;
     };
     TreeSeg seg;
     for (int si = 0; tree_next(walk, p, seg); ++si) {
@@ -758,6 +806,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool any = tile < seg.t1;            // this group has a tile of the item
       if (!any && lane == 0) mbar_arrive(&q_empty[qb]);
       int last = i;                              // its last one
+      bool scales_taken = false;
       for (; begun && tile < seg.t1; tile += kEvery, i += kEvery) {
         last = i;
         const int key = tile * 128 + tid;
@@ -769,7 +818,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (edge && u >= 0) {
           seen = 0ull;
           if (u < seg.drafts) {
-            int t = m0 % p.T;
+            int t = p.T == 1 ? 0 : m0 % p.T;
             const uint8_t* column = p.mask ? p.mask + seg.b * p.mask_stride + u : nullptr;
 #pragma unroll 32
             for (int c = 0; c < kCols; ++c) {
@@ -780,20 +829,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         if (threadIdx.x == 0) FA_TRACE_AT(i, 0);
-        float sk = 1.f, sv = 1.f, lv = 0.f;
+        // (rows past the sequence have no scales; a V scale that is not a size
+        // makes its row's probabilities NaN)
+        float sk_now = 1.f, sv_now = 1.f, lv = 0.f;
         if constexpr (E4M3) {
-          const int ss = i % Lay::kScales;
-          ok = mbar_wait_warp(&sc_full[ss], (i / Lay::kScales) & 1, wc, 71) && ok;
+          if (!scales_taken) ok = take_scales(i) && ok;
+          scales_taken = false;
           if (key < L) {
-            const float* sc = reinterpret_cast<const float*>(smem + Lay::kScale + ss * 1024);
-            sk = sc[tid];
-            sv = sc[128 + tid];
-            if (!(sv >= kTreeMinScale)) sv = sv >= 0.f ? kTreeMinScale : NAN;
-            else if (sv == INFINITY) sv = NAN;
+            sk_now = sk;
+            sv_now = sv;
+            if (!(sv_now >= kTreeMinScale && sv_now < INFINITY))
+              sv_now = sv_now >= 0.f && sv_now < 1.f ? kTreeMinScale : NAN;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_empty[ss]);
-          lv = lg2_approx(sv);
+          lv = lg2_approx(sv_now);
         }
         if (threadIdx.x == 0) FA_TRACE_AT(i, 1);
         ok = wait_s(i, 72) && ok;  // S(i) is complete
@@ -803,9 +851,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // the V scale sv = 2^lv, which multiplies what is stored)
         float d[kCols];
         {
+          const uint32_t tS = tmem + lane_off + (i & 1) * Lay::kSCols + col0;
           uint32_t raw[kCols];
-          tmem_ld_cols<kCols>(tmem + lane_off + (i & 1) * R + col0, raw);
-          const unsigned long long f2 = E4M3 ? f2pack(sk, sk) : f2pack(p.scale_log2, p.scale_log2);
+          tmem_ld_cols<kCols>(tS, raw);
+          if constexpr (Lay::kStackQ) {
+#pragma unroll
+            for (int t = 1; t < Lay::kTermsQ; ++t) {
+              uint32_t more[kCols];
+              tmem_ld_cols<kCols>(tS + t * R, more);
+#pragma unroll
+              for (int c = 0; c < kCols; c += 2) {
+                float lo, hi;
+                f2unpack(fadd2(f2pack(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1])),
+                               f2pack(__uint_as_float(more[c]), __uint_as_float(more[c + 1]))), lo, hi);
+                raw[c] = __float_as_uint(lo);
+                raw[c + 1] = __float_as_uint(hi);
+              }
+            }
+          }
+          const unsigned long long f2 = E4M3 ? f2pack(sk_now, sk_now) : f2pack(p.scale_log2, p.scale_log2);
 #pragma unroll
           for (int c = 0; c < kCols; c += 4) {
             const float4 n4 = *reinterpret_cast<const float4*>(nr + c);
@@ -828,12 +892,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int c = 0; c < kCols; ++c)
             if (!((seen >> c) & 1)) d[c] = -INFINITY;
         }
-        if (E4M3 && !(sv == sv)) {
+        if (E4M3 && !(sv_now == sv_now)) {
           // a V row without a scale makes the rows that see it NaN, and no other
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
             if ((seen >> c) & 1) d[c] = NAN;
-          sv = 0.f;
+          sv_now = 0.f;
           lv = 0.f;
         }
         float top = d[0];
@@ -867,11 +931,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           force = named_bar_or(bar_id, 128, tid < kCols && unset);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            d[c] += move[c];
-            sum[c] *= alpha[c];
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(move + c);
+            d[c] += m4.x;
+            d[c + 1] += m4.y;
+            d[c + 2] += m4.z;
+            d[c + 3] += m4.w;
           }
           if (tile - seg.t0 >= kEvery) {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 4) {
+              const float4 a4 = *reinterpret_cast<const float4*>(alpha + c);
+              sum[c] *= a4.x;
+              sum[c + 1] *= a4.y;
+              sum[c + 2] *= a4.z;
+              sum[c + 3] *= a4.w;
+            }
             // O^T: this thread is row d = tid; the products so far have to be complete
             ok = wait_o(i - kEvery, 73);
             if (!named_bar_and(bar_id, 128, ok)) { ok = false; break; }
@@ -893,6 +968,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         if (threadIdx.x == 0) FA_TRACE_AT(i, 4);
+        if (E4M3 && tile + kEvery < seg.t1) {
+          ok = take_scales(i + kEvery) && ok;
+          scales_taken = true;
+        }
         // the product that read this P buffer before is complete (so V(i - 2), and
         // with it the slot's round before V(i)'s, is known to have come and gone)
         if (i >= Lay::kPBufs) ok = wait_o(i - Lay::kPBufs, 75) && ok;
@@ -937,7 +1016,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         uint8_t* prow = smem + Lay::kP + (i % Lay::kPBufs) * Lay::kPBytes + tid * 128;
         const uint32_t swz = tid & 7;
         constexpr int kStep = kCols < 16 ? 8 : 16;
-        const unsigned long long sv2 = f2pack(sv, sv);
+        const unsigned long long sv2 = f2pack(sv_now, sv_now);
 #pragma unroll
         for (int c = 0; c < kCols; c += kStep) {
           constexpr int kTerms = E4M3 ? Lay::kTermsP : 1;
@@ -1005,8 +1084,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const long long out0 = (static_cast<long long>(seg.b) * p.Hq + static_cast<long long>(seg.hk) * p.group) * p.T;
       // this group finishes columns e0 .. e0 + R / 2
       const int e0 = grp * (R / 2);
+      float stat_l = 0.f, stat_top = 0.f;
       if (tid < R / 2) {
-        const int col = e0 + tid, m = seg.rt * R + col;
+        const int col = e0 + tid;
         auto total = [&](int g, int c) {
           const float* w = s_warp + g * 4 * kCols + c;
           return (w[0] + w[kCols]) + (w[2 * kCols] + w[3 * kCols]);
@@ -1016,7 +1096,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const float l0 = total(0, col), l1 = total(1, col);
           const float r0 = -s_nr[col], r1 = -s_nr[kCols + col];
           top = fmaxf(l0 == 0.f ? -INFINITY : r0, l1 == 0.f ? -INFINITY : r1);
-          const float w0 = l0 == 0.f ? 0.f : exp2f(r0 - top), w1 = l1 == 0.f ? 0.f : exp2f(r1 - top);
+          const float w0 = l0 == 0.f ? 0.f : ex2_approx(r0 - top), w1 = l1 == 0.f ? 0.f : ex2_approx(r1 - top);
           l = (l0 == 0.f ? 0.f : w0 * l0) + (l1 == 0.f ? 0.f : w1 * l1);
           const float inv = !complete ? 1.f : l == 0.f ? 0.f : 1.f / l;
           s_weight[col] = w0 * inv;
@@ -1026,11 +1106,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           top = -nr[tid];
           s_weight[grp * kCols + tid] = l == 0.f ? 0.f : complete ? 1.f / l : 1.f;
         }
-        if (!complete) {
-          reinterpret_cast<float2*>(slot + R * D)[col] = make_float2(top, l);
-        } else if (m < rows_all && m % p.T < seg.drafts) {
-          p.lse[out0 + m] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
-        }
+        stat_l = l;
+        stat_top = top;
       }
       named_bar_sync(bar_id, 128);
       const int fix = s_fix[(si & 1) * 2] | s_fix[(si & 1) * 2 + 1];
@@ -1047,7 +1124,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
           for (int t = 0; t < Lay::kOCols / R; ++t) {
             uint32_t ro[8];
-            tmem_ld8(tmem + lane_off + 2 * R + g * Lay::kOCols + t * R + e0 + c, ro);
+            tmem_ld8(tmem + lane_off + Lay::kTmemO + g * Lay::kOCols + t * R + e0 + c, ro);
 #pragma unroll
             for (int e = 0; e < 8; ++e) og[e] += __uint_as_float(ro[e]);
           }
@@ -1075,17 +1152,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         if (complete) {
-          int t = m % p.T;
+          int t = seg.drafts == p.T ? 0 : m % p.T;
           uint16_t* to = reinterpret_cast<uint16_t*>(p.o) + (out0 + m) * D + tid;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            if (m + e < rows_all && t < seg.drafts)
+            if (m + e < rows_all && (seg.drafts == p.T || t < seg.drafts))
               to[e * D] = static_cast<uint16_t>(pack2<BF16>(o[e], 0.f));
             if (++t == p.T) t = 0;
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) slot[(e0 + c + e) * D + tid] = o[e];
+        }
+      }
+      if (tid < R / 2) {
+        const int col = e0 + tid, m = seg.rt * R + col;
+        if (!complete) {
+          reinterpret_cast<float2*>(slot + R * D)[col] = make_float2(stat_top, stat_l);
+        } else if (m < rows_all && (seg.drafts == p.T || m % p.T < seg.drafts)) {
+          p.lse[out0 + m] = stat_l == 0.f ? -INFINITY : (stat_top + log2f(stat_l)) * 0.69314718055994531f;
         }
       }
       tc_fence_before();
