@@ -99,7 +99,10 @@ struct TreeLayout {
   static constexpr int kStat = kScale + kScales * 1024;
   static constexpr int kBar = kStat + kStatBytes;
   static constexpr int kSmemBytes = kBar + 512 + 1024;      // + slack to align to 1024
-  static constexpr int kOCols = kStack ? kTermsP * R : R;
+  // (3 terms are computed as 4: products with N = 48 or 96 columns take longer
+  // than with 64 or 128, 129 against 124 us for 64 sequences of 4500 keys; the
+  // last quarter is not read)
+  static constexpr int kOCols = kStack ? 4 * R : R;
   static constexpr int kTmemO = 2 * kSCols;                 // S twice, then O
   static constexpr int kTmemUsed = kTmemO + (kTurns ? 2 : 1) * kOCols;
   static_assert(kTmemUsed <= 512, "TMEM columns");
@@ -170,7 +173,8 @@ __device__ __forceinline__ bool tree_next(TreeWalk& w, const TreeParams& p, Tree
 // in tile i for S(i), for O of tile i - 1 or i - 2, and at an item's end for O of
 // its last tile.  No phase can be missed there: with n >= 2 slots the next one
 // of the same slot belongs to S(i + 2), O(i) or a later tile, whose product
-// waits for that very softmax step (both issuing threads go in order).  Nor can
+// waits for that very softmax step or, S(i + 2), for all warps to have read
+// S(i) (both issuing threads go in order).  Nor can
 // a wait be early (a parity wait returns at once while the phase before is still
 // open): whoever waits for a round of a slot has waited for the round before, or
 // for what followed from it.
@@ -261,6 +265,44 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
+}
+// Sums of TERMS sets of 8 columns, STEP columns apart, loaded with one wait.
+template <int TERMS, int STEP>
+__device__ __forceinline__ void tmem_sum8(uint32_t taddr, float (&s)[8]) {
+  uint32_t r[TERMS][8];
+#define FA_LD8(a, b) \
+  "tcgen05.ld.sync.aligned.32x32b.x8.b32 {" a "}, [" b "];\n\t"
+#define FA_OUT8(t) \
+  "=r"(r[t][0]), "=r"(r[t][1]), "=r"(r[t][2]), "=r"(r[t][3]), "=r"(r[t][4]), "=r"(r[t][5]), "=r"(r[t][6]), "=r"(r[t][7])
+  if constexpr (TERMS == 1) {
+    tmem_ld8(taddr, r[0]);
+  } else if constexpr (TERMS == 3) {
+    asm volatile(FA_LD8("%0, %1, %2, %3, %4, %5, %6, %7", "%24")
+                 FA_LD8("%8, %9, %10, %11, %12, %13, %14, %15", "%25")
+                 FA_LD8("%16, %17, %18, %19, %20, %21, %22, %23", "%26")
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : FA_OUT8(0), FA_OUT8(1), FA_OUT8(2)
+                 : "r"(taddr), "r"(taddr + STEP), "r"(taddr + 2 * STEP)
+                 : "memory");
+  } else {
+    static_assert(TERMS == 4, "1, 3 or 4 terms");
+    asm volatile(FA_LD8("%0, %1, %2, %3, %4, %5, %6, %7", "%32")
+                 FA_LD8("%8, %9, %10, %11, %12, %13, %14, %15", "%33")
+                 FA_LD8("%16, %17, %18, %19, %20, %21, %22, %23", "%34")
+                 FA_LD8("%24, %25, %26, %27, %28, %29, %30, %31", "%35")
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : FA_OUT8(0), FA_OUT8(1), FA_OUT8(2), FA_OUT8(3)
+                 : "r"(taddr), "r"(taddr + STEP), "r"(taddr + 2 * STEP), "r"(taddr + 3 * STEP)
+                 : "memory");
+  }
+#undef FA_LD8
+#undef FA_OUT8
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    s[e] = __uint_as_float(r[0][e]);
+#pragma unroll
+    for (int t = 1; t < TERMS; ++t) s[e] += __uint_as_float(r[t][e]);
+  }
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
@@ -356,10 +398,39 @@ __host__ __device__ constexpr size_t tree_slot_floats() {
   return static_cast<size_t>(Lay::R) * (Lay::D + 2);
 }
 
+// Drafted V rows with values that are not finite were cleared for the products:
+// adds those values of column d, of keys k0 .. k1 - 1, to the queries m0 ..
+// m0 + n - 1 that see them (in the output, or in a partial result).
+template <int D, bool BF16, bool E4M3>
+__device__ __noinline__ void tree_add_not_finite(const TreeParams& p, int b, int hk, int ctx, int drafts,
+                                                 int k0, int k1, int m0, int n, int d, float* partial) {
+  uint16_t* o = reinterpret_cast<uint16_t*>(p.o) +
+                ((static_cast<long long>(b) * p.Hq + static_cast<long long>(hk) * p.group) * p.T + m0) * D + d;
+  for (int key = k0; key < k1; ++key) {
+    const long long row = cache_row(p.c, b, hk, key);
+    if (row < 0) continue;
+    float v, skip;
+    if constexpr (E4M3) unpack_e4m3x2(p.c.v[row * D + d], v, skip);
+    else unpack2<BF16>(reinterpret_cast<const uint16_t*>(p.c.v)[row * D + d], v, skip);
+    if (fabsf(v) < INFINITY) continue;
+    for (int e = 0; e < n; ++e) {
+      const int t = (m0 + e) % p.T;
+      if (m0 + e >= p.group * p.T || t >= drafts || !tree_sees(p, b, t, key - ctx)) continue;
+      if (partial != nullptr) {
+        partial[e * D + d] += v;
+      } else {
+        float old;
+        unpack2<BF16>(o[e * D], old, skip);
+        o[e * D] = static_cast<uint16_t>(pack2<BF16>(old + v, 0.f));
+      }
+    }
+  }
+}
+
 template <int D, bool BF16, bool E4M3, int R>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                   const TreeParams p) {
+                   const __grid_constant__ TreeParams p) {
   using Lay = TreeLayout<D, BF16, E4M3, R>;
   constexpr int kCols = Lay::kCols;
   constexpr int kSlots = Lay::kSlots, kSlotsK = Lay::kSlotsK, kSlotsV = Lay::kSlotsV;
@@ -377,7 +448,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint64_t* sc_full = kv_empty + kSlots;        // [8]
   uint64_t* sc_empty = sc_full + 8;             // [8]
   uint64_t* p_full = sc_empty + 8;              // [2]
-  uint64_t* q_full = p_full + 2;                // [2]
+  uint64_t* s_free = p_full + 2;                // [2]
+  uint64_t* q_full = s_free + 2;                // [2]
   uint64_t* q_empty = q_full + 2;               // [2]
   uint64_t* drain = q_empty + 2;                // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
@@ -385,7 +457,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   volatile int* s_fix = abort_flag + 1;         // [2 parities][2 groups]
   TreeWalk* s_walk = reinterpret_cast<TreeWalk*>(const_cast<int*>(s_fix + 4));
   long long* s_scan = reinterpret_cast<long long*>(smem + Lay::kStat);  // setup only, one per warp
-  static_assert(8 * (2 * 12 + 16 + 8) + 4 * 6 + sizeof(TreeWalk) <= 512, "barrier area");
+  static_assert(8 * (2 * 12 + 16 + 10) + 4 * 6 + sizeof(TreeWalk) <= 512, "barrier area");
   static_assert(Lay::kStatBytes >= kTreeThreads / 32 * 8, "scan scratch");
   const WaitCtl wc{abort_flag, p.wait_ns};
 
@@ -403,6 +475,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&p_full[s], Lay::kTurns ? 4 : 8);
+      mbar_init(&s_free[s], Lay::kTurns ? 4 : 8);
       mbar_init(&q_full[s], 3);
       mbar_init(&q_empty[s], 8);
       mbar_init(&drain[s], 1);
@@ -582,7 +655,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t b0 = sdesc_lo(base + Lay::kQ + qb * Lay::kQBytes, false);
         for (int tile = seg.t0; ok && tile < seg.t1; ++tile, ++i) {
           // S(i - 2) has been read
-          if (i >= 2) ok = mbar_wait(&p_full[i & 1], ((i >> 1) - 1) & 1, wc, 65);
+          if (i >= 2) ok = mbar_wait(&s_free[i & 1], ((i >> 1) - 1) & 1, wc, 65);
           // With many rows the products take long, and O(i - 2) is what the softmax
           // waits for next: let it finish first, S(i) has time.
           if (!Lay::kTurns && ok && i >= 2)
@@ -817,10 +890,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         uint64_t seen = ~0ull;
         if (edge && u >= 0) {
           seen = 0ull;
-          if (u < seg.drafts) {
-            int t = p.T == 1 ? 0 : m0 % p.T;
-            const uint8_t* column = p.mask ? p.mask + seg.b * p.mask_stride + u : nullptr;
-#pragma unroll 32
+          const uint8_t* column = p.mask ? p.mask + seg.b * p.mask_stride + u : nullptr;
+          if (u < seg.drafts && p.T == 1) {
+            if (column == nullptr || column[0] != 0) seen = ~0ull;
+          } else if (u < seg.drafts) {
+            int t = m0 % p.T;
+#pragma unroll 16
             for (int c = 0; c < kCols; ++c) {
               const bool sees = column ? column[static_cast<long long>(t) * p.T] != 0 : u <= t;
               seen |= static_cast<uint64_t>(sees) << c;
@@ -869,6 +944,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               }
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[i & 1]);
           const unsigned long long f2 = E4M3 ? f2pack(sk_now, sk_now) : f2pack(p.scale_log2, p.scale_log2);
 #pragma unroll
           for (int c = 0; c < kCols; c += 4) {
@@ -886,6 +964,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             f2unpack(a, d[c], d[c + 1]);
             f2unpack(b, d[c + 2], d[c + 3]);
           }
+        }
+        if (tile + kEvery >= seg.t1) {           // nobody of this warp reads Q's scales again
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_empty[qb]);
         }
         if (edge && u >= 0) {
 #pragma unroll
@@ -952,7 +1034,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (!named_bar_and(bar_id, 128, ok)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
-            for (int t = 0; t < Lay::kOCols / R; ++t) {
+            for (int t = 0; t < (Lay::kStack ? Lay::kTermsP : 1); ++t) {
 #pragma unroll 1
               for (int c = 0; c < kCols; c += 8) {
                 const uint32_t at = tO + t * R + col0 + c;
@@ -982,30 +1064,43 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           ok = mbar_wait_warp(&kv_full[kSlotsK + slot], (i / kSlotsV) & 1, wc, 74) && ok;
           if (ok && u >= 0) {
             uint8_t* row = smem + Lay::kV + slot * Lay::kSlotBytes + tid * 128;
+            // A thread has its key's row, or half of it if the groups share the
+            // tile.  (The lanes start at different 16-byte chunks: rows are 128
+            // bytes apart, so a chunk of 32 rows is in the same banks.  Rarely
+            // executed code is kept short: what it costs is fetching it.)
+            constexpr int kChunks = Lay::kTurns ? 8 : 4;
+            auto chunk = [&](int pn, int ch) {
+              const int at = Lay::kTurns ? (ch + tid) & 7 : grp * 4 + ((ch + tid) & 3);
+              return reinterpret_cast<uint4*>(row + pn * 16384 + at * 16);
+            };
+            if (key >= L) {
 #pragma unroll
-            for (int pn = 0; pn < Lay::kPanels; ++pn) {
-#pragma unroll 4
-              for (int ch = Lay::kTurns ? 0 : grp * 4; ch < (Lay::kTurns ? 8 : grp * 4 + 4); ++ch) {
-                uint4* at = reinterpret_cast<uint4*>(row + pn * 16384 + ch * 16);
-                if (key >= L) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                  uint4 v = *at;
-                  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                  bool found = false;
+              for (int pn = 0; pn < Lay::kPanels; ++pn)
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    uint32_t bad;  // all ones in the elements that are not finite
-                    if constexpr (E4M3) bad = __vcmpeq4(w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                    else if constexpr (BF16) bad = __vcmpeq2(w[e] & 0x7F807F80u, 0x7F807F80u);
-                    else bad = __vcmpeq2(w[e] & 0x7C007C00u, 0x7C007C00u);
-                    found |= bad != 0;
-                    w[e] &= ~bad;
-                  }
-                  if (found) {
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                    s_fix[(si & 1) * 2 + grp] = 1;
-                  }
+                for (int ch = 0; ch < kChunks; ++ch) *chunk(pn, ch) = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              // elements of a word whose exponent is all ones (e4m3: whose code
+              // is NaN) carry into their top bit
+              constexpr uint32_t kMask = E4M3 ? 0x7F7F7F7Fu : BF16 ? 0x7F807F80u : 0x7C007C00u;
+              constexpr uint32_t kOne = E4M3 ? 0x01010101u : BF16 ? 0x00800080u : 0x04000400u;
+              constexpr uint32_t kTop = E4M3 ? 0x80808080u : 0x80008000u;
+              uint32_t bad = 0u;
+#pragma unroll
+              for (int pn = 0; pn < Lay::kPanels; ++pn)
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) {
+                  const uint4 v = *chunk(pn, ch);
+                  bad |= ((v.x & kMask) + kOne) | ((v.y & kMask) + kOne) | ((v.z & kMask) + kOne) |
+                         ((v.w & kMask) + kOne);
+                }
+              if (bad & kTop) {
+                s_fix[(si & 1) * 2 + grp] = 1;
+#pragma unroll 1
+                for (int e = 0; e < Lay::kPanels * kChunks * 4; ++e) {
+                  uint32_t* w = reinterpret_cast<uint32_t*>(chunk(e / (kChunks * 4), e / 4 % kChunks)) + e % 4;
+                  uint32_t clear = ((*w & kMask) + kOne) & kTop;  // top bit of each such element
+                  clear = E4M3 ? (clear >> 7) * 0xFFu : (clear >> 15) * 0xFFFFu;
+                  *w &= ~clear;
                 }
               }
             }
@@ -1065,10 +1160,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&p_full[i & 1]);
-          if (tile + kEvery >= seg.t1) mbar_arrive(&q_empty[qb]);
-        }
+        if (lane == 0) mbar_arrive(&p_full[i & 1]);
         if (threadIdx.x == 0) FA_TRACE_AT(i, 7);
       }
       // ----------------------------------------------------------- end of the item
@@ -1113,21 +1205,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const int fix = s_fix[(si & 1) * 2] | s_fix[(si & 1) * 2 + 1];
 #pragma unroll 1
       for (int c = 0; c < R / 2; c += 8) {
+        if (seg.rt * R + e0 + c >= rows_all) break;  // (no such rows)
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = 0.f;
 #pragma unroll
         for (int g = 0; g < (Lay::kTurns ? 2 : 1); ++g) {
           float og[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) og[e] = 0.f;
-#pragma unroll
-          for (int t = 0; t < Lay::kOCols / R; ++t) {
-            uint32_t ro[8];
-            tmem_ld8(tmem + lane_off + Lay::kTmemO + g * Lay::kOCols + t * R + e0 + c, ro);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) og[e] += __uint_as_float(ro[e]);
-          }
+          tmem_sum8<Lay::kStack ? Lay::kTermsP : 1, R>(
+              tmem + lane_off + Lay::kTmemO + g * Lay::kOCols + e0 + c, og);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             // (weight 0: no key seen, and maybe nothing written there)
@@ -1137,20 +1223,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         if (tid >= D) continue;                  // (d = 64: the upper lanes hold nothing)
         const int m = seg.rt * R + e0 + c;       // first of 8 rows
-        if (fix) {
-          // drafted V rows with values that are not finite were cleared there:
-          // add them for the queries that see them
-          for (int key = max(seg.ctx, seg.t0 * 128); key < min(L, seg.t1 * 128); ++key) {
-            const long long row = cache_row(p.c, seg.b, seg.hk, key);
-            if (row < 0) continue;
-            float v, skip;
-            if constexpr (E4M3) unpack_e4m3x2(p.c.v[row * D + tid], v, skip);
-            else unpack2<BF16>(reinterpret_cast<const uint16_t*>(p.c.v)[row * D + tid], v, skip);
-            if (fabsf(v) < INFINITY) continue;
-            for (int e = 0; e < 8; ++e)
-              if (tree_sees(p, seg.b, (m + e) % p.T, key - seg.ctx)) o[e] += v;
-          }
-        }
         if (complete) {
           int t = seg.drafts == p.T ? 0 : m % p.T;
           uint16_t* to = reinterpret_cast<uint16_t*>(p.o) + (out0 + m) * D + tid;
@@ -1165,6 +1237,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int e = 0; e < 8; ++e) slot[(e0 + c + e) * D + tid] = o[e];
         }
       }
+      if (fix && tid < D)
+        tree_add_not_finite<D, BF16, E4M3>(p, seg.b, seg.hk, seg.ctx, seg.drafts, max(seg.ctx, seg.t0 * 128),
+                                           min(L, seg.t1 * 128), seg.rt * R + e0, R / 2, tid,
+                                           complete ? nullptr : slot + e0 * D);
       if (tid < R / 2) {
         const int col = e0 + tid, m = seg.rt * R + col;
         if (!complete) {
