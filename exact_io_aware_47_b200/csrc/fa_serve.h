@@ -39,14 +39,16 @@ struct CacheView {
   const int32_t* table;      // nullptr: page b for sequence b
   int table_stride;          // pages per sequence (1 without a table)
   int num_pages, page_size, Hk;
+  long long room;            // positions of a sequence: those of the table, below 2^31
+  unsigned page_mul, page_shift;  // x / page_size = umulhi(x, page_mul) >> page_shift, x < 2^31
 };
 
 // Row index (over [num_pages, Hk, page_size]) of position `pos` of sequence b
 // and head h; -1 if the position is past the table or its page is not in the
 // pool.
 __device__ __forceinline__ long long cache_row(const CacheView& c, int b, int h, long long pos) {
-  if (pos < 0 || pos >= static_cast<long long>(c.table_stride) * c.page_size) return -1;
-  const unsigned at = static_cast<unsigned>(pos) / static_cast<unsigned>(c.page_size);
+  if (pos < 0 || pos >= c.room) return -1;
+  const unsigned at = __umulhi(static_cast<unsigned>(pos), c.page_mul) >> c.page_shift;
   const int row = static_cast<int>(pos - static_cast<long long>(at) * c.page_size);
   const int page = c.table ? c.table[static_cast<long long>(b) * c.table_stride + at] : b;
   if (page < 0 || page >= c.num_pages) return -1;
@@ -78,7 +80,6 @@ struct TreeParams {
   float scale_log2;          // scale * log2(e)
   int row_tiles;             // ceil(group * T / rows of a tile)
   int box, box_log2;         // keys of one TMA load: a power of two that divides page_size
-  unsigned page_mul, page_shift;  // x / page_size = umulhi(x, page_mul) >> page_shift, x < 2^31
   int grid;                  // CTAs
   int* heads;                // workspace: [grid][4], see fa_tree_kernel
   float* partial;            // workspace: [grid][2] slots

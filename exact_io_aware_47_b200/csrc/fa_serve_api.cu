@@ -139,6 +139,13 @@ int cache_view(const void* k_cache, const void* v_cache, const float* k_scale,
   c->num_pages = num_pages;
   c->page_size = page_size;
   c->Hk = Hk;
+  c->room = std::min(static_cast<long long>(c->table_stride) * page_size, (1ll << 31) - 1);
+  // 2^(s - 1) < page_size <= 2^s: with m = ceil(2^(31 + s) / page_size) < 2^32 the
+  // error of x m / 2^(31 + s) is below x / 2^(31 + s) < 1 / page_size for x < 2^31
+  int s = 1;
+  while ((1ll << s) < page_size) ++s;
+  c->page_mul = static_cast<unsigned>(((1ull << (31 + s)) + page_size - 1) / page_size);
+  c->page_shift = static_cast<unsigned>(s - 1);
   return FA_OK;
 }
 
@@ -307,12 +314,6 @@ extern "C" int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cac
   p.box_log2 = 7;
   while (page_size % (1 << p.box_log2) != 0) --p.box_log2;  // (page_size is a multiple of 16)
   p.box = 1 << p.box_log2;
-  // 2^(s - 1) < page_size <= 2^s: with m = ceil(2^(31 + s) / page_size) < 2^32 the
-  // error of x m / 2^(31 + s) is below x / 2^(31 + s) < 1 / page_size for x < 2^31
-  int s = 1;
-  while ((1ll << s) < page_size) ++s;
-  p.page_mul = static_cast<unsigned>(((1ull << (31 + s)) + page_size - 1) / page_size);
-  p.page_shift = static_cast<unsigned>(s - 1);
   p.heads = static_cast<int*>(workspace);
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                        round256(kTreeMaxCtas * 4 * sizeof(int)));

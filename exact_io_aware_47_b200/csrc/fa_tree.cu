@@ -117,7 +117,7 @@ struct TreeLens {
 };
 __device__ __forceinline__ TreeLens tree_lens(const TreeParams& p, int b) {
   // (positions stay within 32 bits, with a tile to spare)
-  const long long room = min(static_cast<long long>(p.c.table_stride) * p.c.page_size, (1ll << 31) - 256);
+  const long long room = min(p.c.room, (1ll << 31) - 256);
   const int n_in = p.draft_lens ? p.draft_lens[b] : p.T;
   const int ctx_in = p.ctx_lens[b];
   const int n_cap = static_cast<int>(min(static_cast<long long>(p.T), room));
@@ -207,7 +207,7 @@ struct TreeTiles {
     const int off = (lane >> per) * 128 + (lane & ((1 << per) - 1)) * p.box;
     if (off < min(b.left, b.tiles * 128)) {
       const unsigned key = tile * 128 + off;
-      const unsigned at = __umulhi(key, p.page_mul) >> p.page_shift;   // key / page_size
+      const unsigned at = __umulhi(key, p.c.page_mul) >> p.c.page_shift;   // key / page_size
       b.y = static_cast<int>(key - at * p.c.page_size);
       b.page = p.c.table ? p.c.table[static_cast<long long>(seg.b) * p.c.table_stride + at] : seg.b;
     }

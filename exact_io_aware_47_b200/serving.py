@@ -6,7 +6,9 @@ one scale per row) and ``forward_tree`` (attention of drafted tokens over the
 cache; one token per sequence is ordinary decoding).  As in ``attention``:
 properties of the tensors are checked here, outputs and the workspace are
 allocated with torch, and the library runs on the current CUDA stream of the
-tensors' device.
+tensors' device.  A decoding step makes these calls for a few microseconds of
+GPU work each, so a good call is told by one cheap test per tensor, and what is
+wrong with a bad one is looked for only then.
 
 One decoding step::
 
@@ -23,7 +25,7 @@ import math
 import torch
 
 from . import _lib
-from .attention import _DTYPES, _E4M3, _check_inputs, _on_device, _stream_handle
+from .attention import _DTYPES, _E4M3, _check_inputs, _on_device
 
 _I64x3 = ctypes.c_int64 * 3
 
@@ -83,31 +85,51 @@ def _strides(t):
 
 
 def _check_strided(name, t, shape, dtype, device):
+    if (torch.is_tensor(t) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and t.device == device and t.stride(-1) == 1):
+        return
     if not torch.is_tensor(t) or not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+    raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
-def _int32_arg(name, x, shapes, device):
-    """Device int32 tensor of one of ``shapes``; lists and host tensors are copied."""
+def _check(name, t, shape, dtype, device):
+    if not (torch.is_tensor(t) and t.is_cuda and t.dtype == dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        if t is not None and not torch.is_tensor(t):
+            raise ValueError(f"{name} must be a tensor")
+        _check_inputs({name: t}, shape, dtype, device)
+
+
+def _int32_arg(name, x, shape, device, other=None):
+    """Device int32 tensor of the shape (or the other one); lists and host
+    tensors are copied."""
     if x is None:
         return None
-    _on_device(name, x, device)
-    if not (torch.is_tensor(x) and x.is_cuda and x.dtype == torch.int32 and x.is_contiguous()):
+    if not (torch.is_tensor(x) and x.is_cuda and x.dtype == torch.int32 and x.device == device
+            and x.is_contiguous()):
+        _on_device(name, x, device)
         x = torch.as_tensor(x, dtype=torch.int32).to(device).contiguous()
-    if tuple(x.shape) not in shapes:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {' or '.join(map(str, shapes))}")
+    if x.shape != shape and (other is None or x.shape != other):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}"
+                         + ("" if other is None else f" or {tuple(other)}"))
     return x
 
 
 def _launch(name, device, *args):
-    with torch.cuda.device(device):
-        _lib.check(name, getattr(_lib, name)(*args, _stream_handle(device)))
+    fn = getattr(_lib.load(), name)
+    stream = torch._C._cuda_getCurrentRawStream(device.index) or None
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        _lib.check(name, status)
 
 
 def _rope(name, q, k, inv_freq, positions, interleaved, factor, q_out, k_out):
@@ -120,33 +142,40 @@ def _rope(name, q, k, inv_freq, positions, interleaved, factor, q_out, k_out):
     dev = q.device
     if q.dtype not in _DTYPES:
         raise ValueError("dtype must be bfloat16 or float16")
-    _check_strided("q", q, (B, Hq, N, d), q.dtype, dev)
+    dt = q.dtype
+    shape = (B, Hq, N, d)
+    _check_strided("q", q, shape, dt, dev)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _check_strided("q_out", q_out, shape, dt, dev)
     Hk = 0
+    k_strides = k_out_strides = None
     if k is not None:
-        if k.dim() != 4:
+        if not torch.is_tensor(k) or k.dim() != 4:
             raise ValueError("k must have as many dimensions as q")
         Hk = k.shape[1]
-        _check_strided("k", k, (B, Hk, N, d), q.dtype, dev)
+        shape = (B, Hk, N, d)
+        _check_strided("k", k, shape, dt, dev)
         if k_out is None:
-            k_out = torch.empty((B, Hk, N, d), dtype=q.dtype, device=dev)
-        _check_strided("k_out", k_out, (B, Hk, N, d), q.dtype, dev)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        else:
+            _check_strided("k_out", k_out, shape, dt, dev)
+        k_strides, k_out_strides = _strides(k), _strides(k_out)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
-    _check_strided("q_out", q_out, (B, Hq, N, d), q.dtype, dev)
-    _on_device("inv_freq", inv_freq, dev)
     f = inv_freq
-    if not (torch.is_tensor(f) and f.is_cuda and f.dtype == torch.float64 and f.is_contiguous()):
+    if not (torch.is_tensor(f) and f.is_cuda and f.dtype == torch.float64 and f.device == dev
+            and f.is_contiguous()):
+        _on_device("inv_freq", inv_freq, dev)
         f = torch.as_tensor(f, dtype=torch.float64).to(dev).contiguous()
     if f.dim() != 1:
         raise ValueError("inv_freq must be [rot / 2]")
-    pos = _int32_arg("positions", positions, ((N,), (B, N)), dev)
+    pos = _int32_arg("positions", positions, (N,), dev, (B, N))
     _launch(name, dev, q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out), Hq, _ptr(k),
-            None if k is None else _strides(k), _ptr(k_out),
-            None if k is None else _strides(k_out), Hk, _ptr(pos),
+            k_strides, _ptr(k_out), k_out_strides, Hk, _ptr(pos),
             N if pos is not None and pos.dim() == 2 else 0, f.data_ptr(), B, N, d, 2 * f.numel(),
-            int(bool(interleaved)), float(factor), _DTYPES[q.dtype])
+            int(bool(interleaved)), float(factor), _DTYPES[dt])
     if packed:
         q_out, k_out = q_out[0], None if k_out is None else k_out[0]
     return q_out, k_out
@@ -180,9 +209,11 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, B, device):
     dt = k_cache.dtype
     if dt not in _E4M3 and dt not in _DTYPES:
         raise ValueError("k_cache must be float8_e4m3fn (or uint8 codes), bfloat16 or float16")
-    _check_inputs({"k_cache": k_cache, "v_cache": v_cache}, (P, Hk, page, d), dt, device)
+    _check("k_cache", k_cache, (P, Hk, page, d), dt, device)
+    _check("v_cache", v_cache, (P, Hk, page, d), dt, device)
     if dt in _E4M3:
-        _check_inputs({"k_scale": k_scale, "v_scale": v_scale}, (P, Hk, page), torch.float32, device)
+        _check("k_scale", k_scale, (P, Hk, page), torch.float32, device)
+        _check("v_scale", v_scale, (P, Hk, page), torch.float32, device)
         fmt = _lib.FA_CACHE_E4M3
     else:
         if k_scale is not None or v_scale is not None:
@@ -192,7 +223,7 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, B, device):
     if block_table is not None:
         if not torch.is_tensor(block_table) or block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError(f"block_table must be an int32 tensor [{B}, pages per sequence]")
-        block_table = _int32_arg("block_table", block_table, (tuple(block_table.shape),), device)
+        block_table = _int32_arg("block_table", block_table, block_table.shape, device)
         stride = block_table.shape[1]
     elif P < B:
         raise ValueError("without a block_table sequence b is page b: num_pages >= B")
@@ -219,12 +250,12 @@ def cache_write(k, v, k_cache, v_cache, start=None, lens=None, block_table=None,
         raise ValueError("dtype must be bfloat16 or float16")
     Hk, page, d, fmt, table, stride = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table,
                                                   B, dev)
-    for name, t in (("k", k), ("v", v)):
-        _check_strided(name, t, (B, Hk, N, d), k.dtype, dev)
+    _check_strided("k", k, (B, Hk, N, d), k.dtype, dev)
+    _check_strided("v", v, (B, Hk, N, d), k.dtype, dev)
     if fmt == _lib.FA_CACHE_16 and k_cache.dtype != k.dtype:
         raise ValueError(f"k has dtype {k.dtype}, the cache {k_cache.dtype}")
-    start = _int32_arg("start", start, ((B,),), dev)
-    lens = _int32_arg("lens", lens, ((B,),), dev)
+    start = _int32_arg("start", start, (B,), dev)
+    lens = _int32_arg("lens", lens, (B,), dev)
     _launch("fa_cache_write", dev, k.data_ptr(), _strides(k), v.data_ptr(), _strides(v),
             k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), _ptr(table),
             stride, _ptr(start), _ptr(lens), B, Hk, N, d, k_cache.shape[0], page, fmt,
@@ -253,9 +284,10 @@ def cache_read(k_cache, v_cache, start, n, lens=None, block_table=None, k_scale=
     new = torch.empty if lens is None else torch.zeros
     k_out = new((B, Hk, n, d), dtype=dtype, device=dev) if k_out is None else k_out
     v_out = new((B, Hk, n, d), dtype=dtype, device=dev) if v_out is None else v_out
-    _check_inputs({"k_out": k_out, "v_out": v_out}, (B, Hk, n, d), dtype, dev)
-    start = _int32_arg("start", start, ((B,),), dev)
-    lens = _int32_arg("lens", lens, ((B,),), dev)
+    _check("k_out", k_out, (B, Hk, n, d), dtype, dev)
+    _check("v_out", v_out, (B, Hk, n, d), dtype, dev)
+    start = _int32_arg("start", start, (B,), dev)
+    lens = _int32_arg("lens", lens, (B,), dev)
     _launch("fa_cache_read", dev, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
             _ptr(v_scale), k_out.data_ptr(), v_out.data_ptr(), _ptr(table), stride, _ptr(start),
             _ptr(lens), B, Hk, n, d, k_cache.shape[0], page, fmt, _DTYPES[dtype])
@@ -285,7 +317,7 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
     dev = q.device
     if q.dtype not in _DTYPES:
         raise ValueError("dtype must be bfloat16 or float16")
-    _check_inputs({"q": q}, (B, Hq, T, d), q.dtype, dev)
+    _check("q", q, (B, Hq, T, d), q.dtype, dev)
     Hk, page, dc, fmt, table, stride = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table,
                                                    B, dev)
     if dc != d:
@@ -301,20 +333,20 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
         if draft_lens is not None:
             lse.fill_(-math.inf)
-    _check_inputs({"out": out}, (B, Hq, T, d), q.dtype, dev)
-    _check_inputs({"lse": lse}, (B, Hq, T), torch.float32, dev)
-    ctx = _int32_arg("ctx_lens", ctx_lens, ((B,),), dev)
+    _check("out", out, (B, Hq, T, d), q.dtype, dev)
+    _check("lse", lse, (B, Hq, T), torch.float32, dev)
+    ctx = _int32_arg("ctx_lens", ctx_lens, (B,), dev)
     if ctx is None:
         raise ValueError("ctx_lens is None")
-    drafts = _int32_arg("draft_lens", draft_lens, ((B,),), dev)
+    drafts = _int32_arg("draft_lens", draft_lens, (B,), dev)
     mask = None
     if tree_mask is not None:
-        _on_device("tree_mask", tree_mask, dev)
         mask = tree_mask
-        if not (torch.is_tensor(mask) and mask.is_cuda and mask.is_contiguous()
-                and mask.dtype in (torch.uint8, torch.bool)):
+        if not (torch.is_tensor(mask) and mask.is_cuda and mask.device == dev
+                and mask.dtype in (torch.uint8, torch.bool) and mask.is_contiguous()):
+            _on_device("tree_mask", tree_mask, dev)
             mask = (torch.as_tensor(mask) != 0).to(dev).contiguous()
-        if tuple(mask.shape) not in ((T, T), (B, T, T)):
+        if mask.shape != (T, T) and mask.shape != (B, T, T):
             raise ValueError(f"tree_mask must be [{T}, {T}] or [{B}, {T}, {T}]")
     if workspace is None:
         workspace = torch.empty(tree_workspace_bytes(B, Hq, Hk, T, d), dtype=torch.uint8, device=dev)
