@@ -11,9 +11,8 @@
 //     S^T [keys x R] = K Q^T          A = K tile (K-major), B = Q (K-major)
 //     O^T [d x R]   += V^T P^T        A = V tile (MN-major), B = P^T (MN-major)
 // K and V go from the cache to shared memory by TMA and are read there by the
-// tensor core as they are: an 8-bit cache is never converted.  Instead the
-// 16-bit operand is cut into 8-bit terms, which one kind::f8f6f4 product sums
-// exactly in fp32:
+// tensor core as they are.  With an 8-bit cache the 16-bit operand is cut into
+// 8-bit terms, whose kind::f8f6f4 products add up exactly in fp32:
 //   * Q, scaled per row by a power of two to [128, 256): e4m3 terms (4
 //     significant bits each), 2 for bf16 (8 bits), 3 for fp16 (11 bits); what
 //     falls below the last term is at most 2^-17 of the row's largest value;
@@ -21,6 +20,9 @@
 //     an fp16 value (3 bits each, down to steps of 2^-16 below a reference at
 //     2^11, so that small probabilities are not lost beside a large one): 3
 //     terms, rounded at the end (9 bits, finer than bf16), or all 4 (exact).
+//   With 64 rows and more, where the softmax's instructions and the products
+//   weigh more than the cache, P stays fp16 and three warps that have time
+//   convert V to fp16 (exact; half the products and no terms to cut).
 // The scale of a K row multiplies its row of S^T, the scale of a V row its
 // row of P^T: both are one thread's.
 //
@@ -37,7 +39,7 @@
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warps 8 and 9
 // load K and V (TMA), warp 12 the scales, warp 10 issues the products of S, warp
-// 11 those of O, warps 13-15 prepare Q.
+// 11 those of O, warps 13-15 prepare Q (and convert V).
 // An issuing thread pays about 60 cycles for an MMA and 210 for a commit
 // (measured, whatever the size), so S and O have a thread each, and there is
 // one commit per product: the barrier that gives a K or V slot back to the
@@ -66,43 +68,51 @@ struct TreeLayout {
   static constexpr bool kTurns = R <= 32;                   // the groups take turns at the tiles
   static constexpr int kCols = kTurns ? R : R / 2;          // columns of a softmax thread
   static constexpr int kTermsQ = E4M3 ? (BF16 ? 2 : 3) : 1;
-  static constexpr int kTermsP = E4M3 ? (BF16 ? 3 : 4) : 1;
+  // e4m3, many rows: V is converted to fp16 in shared memory (exact) and P is
+  // fp16, see the top
+  static constexpr bool kConvert = E4M3 && !kTurns;
+  static constexpr bool kTerms8 = E4M3 && kTurns;           // P in e5m2 terms
+  static constexpr int kTermsP = kTerms8 ? (BF16 ? 3 : 4) : 1;
   static constexpr int kPanels = (D * (E4M3 ? 1 : 2) + 127) / 128;  // 128-byte panels of a row
   static constexpr int kPanelElems = E4M3 ? 128 : 64;
   static constexpr int kSlotBytes = kPanels * 16384;
   static constexpr int kSteps = D * (E4M3 ? 1 : 2) / 32;    // MMAs of 32 bytes over d
-  // up to 64 rows the terms of P sit side by side (one product of N = terms x R
-  // columns, summed at the end); with 128 rows each has its own panel and its
-  // own product into the same columns
-  static constexpr bool kStack = E4M3 && R < 128;
-  static constexpr bool kStackQ = kTurns && kTermsQ > 1;    // the terms of Q likewise
+  // with few rows the terms of Q and of P sit side by side (one product of N =
+  // terms x R columns, summed afterwards); with many rows the terms of Q are
+  // products into the same columns
+  static constexpr bool kStackQ = kTurns && kTermsQ > 1;
   static constexpr int kSCols = kStackQ ? kTermsQ * R : R;
-  static constexpr int kPRow = E4M3 ? kTermsP * R : 2 * R;  // bytes of a key's row of P^T
+  static constexpr int kPRow = kTerms8 ? kTermsP * R : 2 * R;  // bytes of a key's row of P^T
   static constexpr int kPBytes = (kPRow + 127) / 128 * 16384;
   static constexpr int kPBufs = R == 128 ? 1 : 2;
   static constexpr int kQPanel = R * 128;
   static constexpr int kQBytes = kTermsQ * kPanels * kQPanel;
   static constexpr int kQBufs = R == 128 ? 1 : 2;
   static constexpr int kScales = E4M3 ? 8 : 0;              // ring of tile scales, 1 KB each
+  static constexpr int kV16Bufs = kConvert ? 2 : 0;         // converted V tiles
+  static constexpr int kV16Bytes = (D + 63) / 64 * 16384;
   // per row: Q scales; per group and column: reference, its last change and
   // factor, final weight; per softmax warp and column: one value
   static constexpr int kStatBytes = (kQBufs * R + 2 * kCols * 4 + 8 * kCols + R) * 4;
-  static constexpr int kFixed = kPBufs * kPBytes + kQBufs * kQBytes + kScales * 1024 + kStatBytes + 512 + 1024;
+  static constexpr int kBarBytes = 640;
+  static constexpr int kFixed = kV16Bufs * kV16Bytes + kPBufs * kPBytes + kQBufs * kQBytes + kScales * 1024 +
+                                kStatBytes + kBarBytes + 1024;
   static constexpr int kSlotsFit = (232448 - kFixed) / kSlotBytes;
   static constexpr int kSlots = kSlotsFit < 12 ? kSlotsFit : 12;
   static constexpr int kSlotsK = kSlots / 2, kSlotsV = kSlots - kSlotsK;  // two rings
   static_assert(kSlotsK >= 2, "a slot is reused two tiles later at the earliest (see below)");
   static constexpr int kV = kSlotsK * kSlotBytes;
-  static constexpr int kP = kSlots * kSlotBytes;
+  static constexpr int kV16 = kSlots * kSlotBytes;
+  static constexpr int kP = kV16 + kV16Bufs * kV16Bytes;
   static constexpr int kQ = kP + kPBufs * kPBytes;
   static constexpr int kScale = kQ + kQBufs * kQBytes;
   static constexpr int kStat = kScale + kScales * 1024;
   static constexpr int kBar = kStat + kStatBytes;
-  static constexpr int kSmemBytes = kBar + 512 + 1024;      // + slack to align to 1024
+  static constexpr int kSmemBytes = kBar + kBarBytes + 1024;  // + slack to align to 1024
   // (3 terms are computed as 4: products with N = 48 or 96 columns take longer
   // than with 64 or 128, 129 against 124 us for 64 sequences of 4500 keys; the
   // last quarter is not read)
-  static constexpr int kOCols = kStack ? 4 * R : R;
+  static constexpr int kOCols = kTerms8 ? 4 * R : R;
   static constexpr int kTmemO = 2 * kSCols;                 // S twice, then O
   static constexpr int kTmemUsed = kTmemO + (kTurns ? 2 : 1) * kOCols;
   static_assert(kTmemUsed <= 512, "TMEM columns");
@@ -361,6 +371,18 @@ __device__ __forceinline__ void unpack_e4m3x2(uint32_t pair, float& lo, float& h
   unpack2<false>(half2, lo, hi);
 }
 
+// Pairs between fp16 and e4m3.
+__device__ __forceinline__ uint32_t pack_e4m3x2_f16(uint32_t half2) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(half2));
+  return static_cast<uint32_t>(r);
+}
+__device__ __forceinline__ uint32_t unpack_e4m3x2_f16(uint32_t pair) {
+  uint32_t half2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(static_cast<unsigned short>(pair)));
+  return half2;
+}
+
 __device__ __forceinline__ uint32_t hsub2_bits(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -451,13 +473,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint64_t* s_free = p_full + 2;                // [2]
   uint64_t* q_full = s_free + 2;                // [2]
   uint64_t* q_empty = q_full + 2;               // [2]
-  uint64_t* drain = q_empty + 2;                // [2]
+  uint64_t* v16_full = q_empty + 2;             // [2]
+  uint64_t* v16_empty = v16_full + 2;           // [2]
+  uint64_t* drain = v16_empty + 2;              // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_fix = abort_flag + 1;         // [2 parities][2 groups]
-  TreeWalk* s_walk = reinterpret_cast<TreeWalk*>(const_cast<int*>(s_fix + 4));
+  volatile int* s_fix = abort_flag + 1;         // [4 items][4 warps or groups that look]
+  TreeWalk* s_walk = reinterpret_cast<TreeWalk*>(const_cast<int*>(s_fix + 16));
   long long* s_scan = reinterpret_cast<long long*>(smem + Lay::kStat);  // setup only, one per warp
-  static_assert(8 * (2 * 12 + 16 + 10) + 4 * 6 + sizeof(TreeWalk) <= 512, "barrier area");
+  static_assert(8 * (2 * kSlots + 16 + 14) + 4 * 18 + sizeof(TreeWalk) <= Lay::kBarBytes, "barrier area");
   static_assert(Lay::kStatBytes >= kTreeThreads / 32 * 8, "scan scratch");
   const WaitCtl wc{abort_flag, p.wait_ns};
 
@@ -467,7 +491,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], Lay::kConvert && s >= kSlotsK ? 3 : 1);
     }
     for (int s = 0; s < 8; ++s) {
       mbar_init(&sc_full[s], 1);
@@ -478,6 +502,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       mbar_init(&s_free[s], Lay::kTurns ? 4 : 8);
       mbar_init(&q_full[s], 3);
       mbar_init(&q_empty[s], 8);
+      mbar_init(&v16_full[s], 3);
+      mbar_init(&v16_empty[s], 1);
       mbar_init(&drain[s], 1);
     }
     *abort_flag = 0;
@@ -659,7 +685,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // With many rows the products take long, and O(i - 2) is what the softmax
           // waits for next: let it finish first, S(i) has time.
           if (!Lay::kTurns && ok && i >= 2)
-            ok = mbar_wait(&kv_empty[kSlotsK + (i - 2) % kSlotsV], ((i - 2) / kSlotsV) & 1, wc, 77);
+            ok = Lay::kConvert ? mbar_wait(&v16_empty[i & 1], ((i >> 1) - 1) & 1, wc, 77)
+                               : mbar_wait(&kv_empty[kSlotsK + (i - 2) % kSlotsV], ((i - 2) / kSlotsV) & 1, wc, 77);
           if (ok) ok = mbar_wait(&kv_full[slot], round & 1, wc, 66);
           if (!ok) break;
           tc_fence_after();
@@ -689,37 +716,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   } else if (warp == 11) {
     // ------------------------------------------------------------- O^T += V^T P^T
     if (lane == 0 && n_tiles > 0) {
-      // both operands MN-major; e4m3 caches: A is e4m3, B e5m2 (format 1)
-      constexpr uint32_t kFormat = E4M3 ? 0u : (BF16 ? 1u : 0u);
-      constexpr uint32_t kIdesc = (1u << 4) | (kFormat << 7) | ((E4M3 ? 1u : kFormat) << 10) |
-                                  (1u << 15) | (1u << 16) |
+      // both operands MN-major; e4m3 caches: A is e4m3 and B e5m2 (format 1), or
+      // both are fp16
+      constexpr bool k8 = Lay::kTerms8;
+      constexpr uint32_t kFormatA = E4M3 ? 0u : (BF16 ? 1u : 0u), kFormatB = k8 ? 1u : kFormatA;
+      constexpr uint32_t kIdesc = (1u << 4) | (kFormatA << 7) | (kFormatB << 10) | (1u << 15) | (1u << 16) |
                                   (static_cast<uint32_t>(Lay::kOCols >> 3) << 17) | (8u << 24);
-      constexpr int kKeySteps = E4M3 ? 4 : 8;                  // 32 or 16 keys each
-      constexpr uint32_t kKeyStep = E4M3 ? 256u : 128u;        // x 16 bytes
-      constexpr int kTerms = E4M3 && !Lay::kStack ? Lay::kTermsP : 1;
+      constexpr int kKeySteps = k8 ? 4 : 8;                    // 32 or 16 keys each
+      constexpr uint32_t kKeyStep = k8 ? 256u : 128u;          // x 16 bytes
       const uint32_t base = smem_addr(smem);
       TreeSeg seg;
       int i = 0, slot = 0, round = 0;
       bool ok = true;
       while (ok && tree_next(walk, p, seg)) {
         for (int tile = seg.t0; tile < seg.t1; ++tile, ++i) {
-          ok = mbar_wait(&kv_full[kSlotsK + slot], round & 1, wc, 67);
+          uint64_t* full = Lay::kConvert ? &v16_full[i & 1] : &kv_full[kSlotsK + slot];
+          ok = mbar_wait(full, Lay::kConvert ? (i >> 1) & 1 : round & 1, wc, 67);
           if (ok) ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, wc, 68);
           if (!ok) break;
           FA_TRACE_AT(i, 17);
           tc_fence_after();
-          const uint32_t a0 = sdesc_lo(base + Lay::kV + slot * Lay::kSlotBytes, true);
+          const uint32_t a0 = sdesc_lo(base + (Lay::kConvert ? Lay::kV16 + (i & 1) * Lay::kV16Bytes
+                                                             : Lay::kV + slot * Lay::kSlotBytes), true);
           const uint32_t b0 = sdesc_lo(base + Lay::kP + (i % Lay::kPBufs) * Lay::kPBytes, true);
           const uint32_t d = tmem + Lay::kTmemO + (Lay::kTurns ? (i & 1) * Lay::kOCols : 0);
           const bool first = tile - seg.t0 < (Lay::kTurns ? 2 : 1);
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-#pragma unroll
-            for (int k = 0; k < kKeySteps; ++k)
-              tree_mma<E4M3>(d, a0 + k * kKeyStep, b0 + t * 1024 + k * kKeyStep, kIdesc,
-                             !first || t + k > 0);
-          }
-          umma_commit(&kv_empty[kSlotsK + slot]);
+          for (int k = 0; k < kKeySteps; ++k)
+            tree_mma<k8>(d, a0 + k * kKeyStep, b0 + k * kKeyStep, kIdesc, !first || k > 0);
+          umma_commit(Lay::kConvert ? &v16_empty[i & 1] : &kv_empty[kSlotsK + slot]);
           if (++slot == kSlotsV) {
             slot = 0;
             ++round;
@@ -739,9 +764,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     constexpr int kIters = (R + 3 * kRowsWarp - 1) / (3 * kRowsWarp);  // of 3 warps x kRowsWarp rows
     constexpr int kBatch = kIters < 8 ? kIters : 8;
     const int sub = lane / kLanes, l = lane % kLanes;
-    TreeSeg seg;
     bool ok = true;
-    for (int si = 0; ok && tree_next(walk, p, seg); ++si) {
+    TreeWalk walk_q = walk;
+    int si = 0;                                  // items whose Q is prepared
+    auto prepare_q = [&]() {
+      TreeSeg seg;
+      if (!tree_next(walk_q, p, seg)) return false;
       const int qb = si % Lay::kQBufs;
       const long long row0 = (static_cast<long long>(seg.b) * p.Hq + static_cast<long long>(seg.hk) * p.group) * p.T +
                              static_cast<long long>(seg.rt) * R;
@@ -759,7 +787,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         if (it0 == 0) {
           ok = mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 69);
-          if (!ok) break;
+          if (!ok) return false;
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -772,31 +800,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int o = kLanes / 2; o > 0; o >>= 1)
             amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           unpack8<BF16>(x, f);
-          // up = 2^(7 - e), e the exponent of amax: amax up in [128, 256)
+          // up = 2^(7 - e), e the exponent of amax: amax up in [128, 256); the
+          // scaled row is exact in fp16 (down to its steps of 2^-24)
           const int e = amax > 0.f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23), 8), 253) : 134;
           const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
           const float down = __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
           if (l == 0 && r < R)
             s_qs[qb * R + r] = amax < INFINITY ? down * p.scale_log2 : __int_as_float(0x7fffffff);
+          uint32_t h[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= up;
+          for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(f[2 * i] * up, f[2 * i + 1] * up);
 #pragma unroll
           for (int t = 0; t < Lay::kTermsQ; ++t) {
-            uint32_t w[2];
-            w[0] = pack_e4m3x4(f[0], f[1], f[2], f[3]);
-            w[1] = pack_e4m3x4(f[4], f[5], f[6], f[7]);
-            if (t + 1 < Lay::kTermsQ) {
+            uint32_t w[4];                       // pairs of codes
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float a, b;
-                unpack_e4m3x2(w[i >> 1] >> (16 * (i & 1)), a, b);
-                f[2 * i] -= a;
-                f[2 * i + 1] -= b;
-              }
+            for (int i = 0; i < 4; ++i) {
+              w[i] = pack_e4m3x2_f16(h[i]);
+              if (t + 1 < Lay::kTermsQ) h[i] = hsub2_bits(h[i], unpack_e4m3x2_f16(w[i]));
             }
             // 8 bytes at column 8 l of row r: chunk l / 2, swizzled by the row
             const uint32_t at = r * 128 + ((((l >> 1) ^ (r & 7)) << 4) | ((l & 1) << 3));
-            if (r < R) *reinterpret_cast<uint2*>(qdst + t * Lay::kQPanel + at) = make_uint2(w[0], w[1]);
+            if (r < R)
+              *reinterpret_cast<uint2*>(qdst + t * Lay::kQPanel + at) =
+                  make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
           }
         } else {
           const uint32_t at = (l >> 3) * Lay::kQPanel + r * 128 + (((l & 7) ^ (r & 7)) << 4);
@@ -804,10 +830,80 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         }
       }
-      if (!ok) break;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
+      ++si;
+      return true;
+    };
+    if constexpr (!Lay::kConvert) {
+      while (prepare_q()) {
+      }
+    } else {
+      // The same warps convert V: Q of the first items, then V of an item and Q of
+      // the next one whose buffer that item's end gives back (never Q before the
+      // V that its buffer waits for).
+#pragma unroll 1
+      for (int q = 0; q < Lay::kQBufs && prepare_q(); ++q) {
+      }
+      TreeSeg seg;
+      int i = 0, slot = 0, round = 0;
+      for (int item = 0; ok && tree_next(walk, p, seg); ++item) {
+        const int L = seg.ctx + seg.drafts;
+        volatile int* fix = s_fix + (item & 3) * 4 + warp - 13;
+        if (lane == 0) *fix = 0;
+        __syncwarp();
+        for (int tile = seg.t0; tile < seg.t1; ++tile, ++i) {
+          ok = mbar_wait_warp(&kv_full[kSlotsK + slot], round & 1, wc, 78);
+          if (ok && i >= 2) ok = mbar_wait_warp(&v16_empty[i & 1], ((i >> 1) - 1) & 1, wc, 79);
+          if (!ok) break;
+          const uint8_t* from = smem + Lay::kV + slot * Lay::kSlotBytes;
+          uint8_t* to = smem + Lay::kV16 + (i & 1) * Lay::kV16Bytes;
+          const bool edge = tile * 128 + 128 > seg.ctx;
+          bool found = false;
+          // a unit: 16 columns of 32 rows, a row per lane
+#pragma unroll 2
+          for (int unit = warp - 13; unit < 4 * (D / 16); unit += 3) {
+            const int row = (unit & 3) * 32 + lane, ch = unit >> 2, sw = row & 7;
+            uint4 v = *reinterpret_cast<const uint4*>(from + row * 128 + ((ch ^ sw) << 4));
+            if (edge) {
+              const int key = tile * 128 + row;
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              if (key >= L) {                    // not in the cache
+                w[0] = w[1] = w[2] = w[3] = 0u;
+              } else if (key >= seg.ctx) {       // drafted: NaN codes apart (tree_add_not_finite)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t nan = ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  found |= nan != 0;
+                  w[e] &= ~((nan >> 7) * 0xFFu);
+                }
+              }
+              v = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            uint32_t h[8];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = unpack_e4m3x2_f16(w[e >> 1] >> (16 * (e & 1)));
+            uint8_t* out = to + (ch >> 2) * 16384 + row * 128;
+            const int c16 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(out + ((c16 ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(out + (((c16 + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          if (found) *fix = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v16_full[i & 1]);
+            mbar_arrive(&kv_empty[kSlotsK + slot]);
+          }
+          if (++slot == kSlotsV) {
+            slot = 0;
+            ++round;
+          }
+        }
+        if (ok) prepare_q();
+      }
     }
     __syncwarp();
   }
@@ -827,8 +923,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // a row's reference stands for P = 2^kBias, and moves when P would pass
     // 2^kOver.  e5m2 terms reach from 2^15 down to steps of 2^-16: the reference
     // at 2^11 leaves 2^4 above it and 2^-27 below; fp16 has steps of 2^-24.
-    constexpr float kBias = E4M3 ? 11.f : BF16 ? 0.f : 7.f;
-    constexpr float kOver = E4M3 ? 15.f : kBias + 8.f;
+    constexpr float kBias = Lay::kTerms8 ? 11.f : (BF16 && !E4M3) ? 0.f : 7.f;
+    constexpr float kOver = Lay::kTerms8 ? 15.f : kBias + 8.f;
     const int rows_all = p.group * p.T;
     bool ok = true;
     int i = 0;                                   // tile of this CTA
@@ -837,7 +933,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       return mbar_wait_warp(&kv_empty[i % kSlotsK], (i / kSlotsK) & 1, wc, site);
     };
     auto wait_o = [&](int i, unsigned site) {
-      return mbar_wait_warp(&kv_empty[kSlotsK + i % kSlotsV], (i / kSlotsV) & 1, wc, site);
+      if constexpr (Lay::kConvert) return mbar_wait_warp(&v16_empty[i & 1], (i >> 1) & 1, wc, site);
+      else return mbar_wait_warp(&kv_empty[kSlotsK + i % kSlotsV], (i / kSlotsV) & 1, wc, site);
     };
     // scales of this thread's row in tile i, taken from the ring while the tile
     // before is worked at
@@ -861,7 +958,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       ok = mbar_wait_warp(&q_full[qb], (si / Lay::kQBufs) & 1, wc, 70) && ok;
       if (tid < kCols) nr[tid] = 0.f;
       bool unset = true;                         // tid < kCols: column tid has no reference yet
-      if (tid == 0) s_fix[(si & 1) * 2 + grp] = 0;
+      if (tid == 0 && !Lay::kConvert) s_fix[(si & 3) * 4 + grp] = 0;
       // (a wait that gave up: this group goes on to the vote at the item's end)
       ok = named_bar_and(bar_id, 128, ok);
       const bool begun = ok;
@@ -1034,7 +1131,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (!named_bar_and(bar_id, 128, ok)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
-            for (int t = 0; t < (Lay::kStack ? Lay::kTermsP : 1); ++t) {
+            for (int t = 0; t < Lay::kTermsP; ++t) {
 #pragma unroll 1
               for (int c = 0; c < kCols; c += 8) {
                 const uint32_t at = tO + t * R + col0 + c;
@@ -1058,8 +1155,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // with it the slot's round before V(i)'s, is known to have come and gone)
         if (i >= Lay::kPBufs) ok = wait_o(i - Lay::kPBufs, 75) && ok;
         // V rows that the cache does not hold are cleared (0 x NaN is NaN), and
-        // drafted rows are searched for values that are not finite
-        if (edge) {
+        // drafted rows are searched for values that are not finite (where V is
+        // converted, that is done there)
+        if (edge && !Lay::kConvert) {
           const int slot = i % kSlotsV;
           ok = mbar_wait_warp(&kv_full[kSlotsK + slot], (i / kSlotsV) & 1, wc, 74) && ok;
           if (ok && u >= 0) {
@@ -1094,7 +1192,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                          ((v.w & kMask) + kOne);
                 }
               if (bad & kTop) {
-                s_fix[(si & 1) * 2 + grp] = 1;
+                s_fix[(si & 3) * 4 + grp] = 1;
 #pragma unroll 1
                 for (int e = 0; e < Lay::kPanels * kChunks * 4; ++e) {
                   uint32_t* w = reinterpret_cast<uint32_t*>(chunk(e / (kChunks * 4), e / 4 % kChunks)) + e % 4;
@@ -1114,7 +1212,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const unsigned long long sv2 = f2pack(sv_now, sv_now);
 #pragma unroll
         for (int c = 0; c < kCols; c += kStep) {
-          constexpr int kTerms = E4M3 ? Lay::kTermsP : 1;
+          constexpr int kTerms = Lay::kTermsP;
           uint32_t w[kTerms][kStep / 4];          // e5m2 terms, four columns a word
           uint32_t h[kStep / 2];                  // 16-bit pairs
 #pragma unroll
@@ -1128,21 +1226,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               if (E4M3) x = fmul2(x, sv2);
               f2unpack(x, pr[o], pr[o + 1]);
             }
-            if constexpr (E4M3) {
+            if constexpr (Lay::kTerms8) {
               uint32_t q[kTerms];
               e5m2_terms<kTerms>(pr[0], pr[1], pr[2], pr[3], q);
 #pragma unroll
               for (int t = 0; t < kTerms; ++t) w[t][e / 4] = q[t];
             } else {
-              h[e / 2] = pack2<BF16>(pr[0], pr[1]);
-              h[e / 2 + 1] = pack2<BF16>(pr[2], pr[3]);
+              h[e / 2] = pack2<BF16 && !E4M3>(pr[0], pr[1]);
+              h[e / 2 + 1] = pack2<BF16 && !E4M3>(pr[2], pr[3]);
             }
           }
           // kStep columns of the key's row of P^T, in 16-byte chunks swizzled by the row
           auto chunk = [&](int byte) {
             return prow + (byte >> 7) * 16384 + ((((byte >> 4) & 7) ^ swz) << 4) + (byte & 15);
           };
-          if constexpr (E4M3) {
+          if constexpr (Lay::kTerms8) {
 #pragma unroll
             for (int t = 0; t < kTerms; ++t) {
               uint8_t* to = chunk(t * R + col0 + c);
@@ -1202,7 +1300,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         stat_top = top;
       }
       named_bar_sync(bar_id, 128);
-      const int fix = s_fix[(si & 1) * 2] | s_fix[(si & 1) * 2 + 1];
+      const volatile int* found = s_fix + (si & 3) * 4;
+      const int fix = found[0] | found[1] | (Lay::kConvert ? found[2] : 0);
 #pragma unroll 1
       for (int c = 0; c < R / 2; c += 8) {
         if (seg.rt * R + e0 + c >= rows_all) break;  // (no such rows)
@@ -1212,7 +1311,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
         for (int g = 0; g < (Lay::kTurns ? 2 : 1); ++g) {
           float og[8];
-          tmem_sum8<Lay::kStack ? Lay::kTermsP : 1, R>(
+          tmem_sum8<Lay::kTermsP, R>(
               tmem + lane_off + Lay::kTmemO + g * Lay::kOCols + e0 + c, og);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
