@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     constexpr int kRowsWarp = 32 / kLanes;
     const int rows_all = p.group * p.T;
     constexpr int kIters = (R + 3 * kRowsWarp - 1) / (3 * kRowsWarp);  // of 3 warps x kRowsWarp rows
-    constexpr int kBatch = kIters < 8 ? kIters : 8;
+    constexpr int kBatch = kIters < 4 ? kIters : 4;
     const int sub = lane / kLanes, l = lane % kLanes;
     bool ok = true;
     TreeWalk walk_q = walk;
@@ -774,20 +774,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const long long row0 = (static_cast<long long>(seg.b) * p.Hq + static_cast<long long>(seg.hk) * p.group) * p.T +
                              static_cast<long long>(seg.rt) * R;
       uint8_t* qdst = smem + Lay::kQ + qb * Lay::kQBytes;
+      // a batch of loads ahead of the rows that are worked at, the first ones
+      // before the buffer is free
+      auto load = [&](int it) {
+        const int r = (it * 3 + warp - 13) * kRowsWarp + sub;
+        return r < R && seg.rt * R + r < rows_all
+                   ? *(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D * 2) + l)
+                   : make_uint4(0u, 0u, 0u, 0u);
+      };
+      uint4 next[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) next[k] = load(k);
+      ok = mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 69);
+      if (!ok) return false;
 #pragma unroll 1
       for (int it0 = 0; it0 < kIters; it0 += kBatch) {
-        // a batch of loads in flight, the first one before the buffer is free
         uint4 xs[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          const int r = ((it0 + k) * 3 + warp - 13) * kRowsWarp + sub;
-          xs[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < R && seg.rt * R + r < rows_all)
-            xs[k] = *(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D * 2) + l);
-        }
-        if (it0 == 0) {
-          ok = mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 69);
-          if (!ok) return false;
+          xs[k] = next[k];
+          next[k] = load(it0 + kBatch + k);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -795,10 +801,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint4 x = xs[k];
         if constexpr (E4M3) {
           float f[8];
-          float amax = abs_max8(x, BF16, 0.f);
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1)
-            amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const float amax = row_amax<kLanes, BF16>(x);
           unpack8<BF16>(x, f);
           // up = 2^(7 - e), e the exponent of amax: amax up in [128, 256); the
           // scaled row is exact in fp16 (down to its steps of 2^-24)
@@ -1087,11 +1090,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (named_bar_or(bar_id, 128, top > kOver || force || !ok)) {
           // some row's reference moves (or a wait gave up)
           if (!named_bar_and(bar_id, 128, ok)) { ok = false; break; }
-          {
-            float m[kCols];
+          constexpr int kPart = kCols < 32 ? kCols : 32;  // (registers)
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) m[c] = d[c] + lv;
-            reduce_columns<kCols, true>(m, lane, s_warp + warp * kCols);
+          for (int part = 0; part < kCols; part += kPart) {
+            float m[kPart];
+#pragma unroll
+            for (int c = 0; c < kPart; ++c) m[c] = d[part + c] + lv;
+            reduce_columns<kPart, true>(m, lane, s_warp + warp * kCols + part);
           }
           named_bar_sync(bar_id, 128);
           if (tid < kCols) {
@@ -1302,38 +1307,53 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       named_bar_sync(bar_id, 128);
       const volatile int* found = s_fix + (si & 3) * 4;
       const int fix = found[0] | found[1] | (Lay::kConvert ? found[2] : 0);
+      constexpr int kOut = Lay::kTurns ? 8 : 16;  // columns at a time
 #pragma unroll 1
-      for (int c = 0; c < R / 2; c += 8) {
+      for (int c = 0; c < R / 2; c += kOut) {
         if (seg.rt * R + e0 + c >= rows_all) break;  // (no such rows)
-        float o[8];
+        float o[kOut];
+        if constexpr (!Lay::kTurns) {
+          uint32_t ro[kOut];
+          tmem_ld_cols<kOut>(tmem + lane_off + Lay::kTmemO + e0 + c, ro);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+          for (int e = 0; e < kOut; e += 4) {
+            // (weight 0: no key seen)
+            const float4 w = *reinterpret_cast<const float4*>(s_weight + e0 + c + e);
+            o[e] = w.x == 0.f ? 0.f : w.x * __uint_as_float(ro[e]);
+            o[e + 1] = w.y == 0.f ? 0.f : w.y * __uint_as_float(ro[e + 1]);
+            o[e + 2] = w.z == 0.f ? 0.f : w.z * __uint_as_float(ro[e + 2]);
+            o[e + 3] = w.w == 0.f ? 0.f : w.w * __uint_as_float(ro[e + 3]);
+          }
+        } else {
 #pragma unroll
-        for (int g = 0; g < (Lay::kTurns ? 2 : 1); ++g) {
+        for (int e = 0; e < kOut; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
           float og[8];
           tmem_sum8<Lay::kTermsP, R>(
               tmem + lane_off + Lay::kTmemO + g * Lay::kOCols + e0 + c, og);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             // (weight 0: no key seen, and maybe nothing written there)
-            const float w = Lay::kTurns ? s_weight[g * kCols + e0 + c + e] : s_weight[e0 + c + e];
+            const float w = s_weight[g * kCols + e0 + c + e];
             o[e] += w == 0.f ? 0.f : w * og[e];
           }
         }
+        }
         if (tid >= D) continue;                  // (d = 64: the upper lanes hold nothing)
-        const int m = seg.rt * R + e0 + c;       // first of 8 rows
+        const int m = seg.rt * R + e0 + c;       // first of kOut rows
         if (complete) {
           int t = seg.drafts == p.T ? 0 : m % p.T;
           uint16_t* to = reinterpret_cast<uint16_t*>(p.o) + (out0 + m) * D + tid;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < kOut; ++e) {
             if (m + e < rows_all && (seg.drafts == p.T || t < seg.drafts))
               to[e * D] = static_cast<uint16_t>(pack2<BF16>(o[e], 0.f));
             if (++t == p.T) t = 0;
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) slot[(e0 + c + e) * D + tid] = o[e];
+          for (int e = 0; e < kOut; ++e) slot[(e0 + c + e) * D + tid] = o[e];
         }
       }
       if (fix && tid < D)
