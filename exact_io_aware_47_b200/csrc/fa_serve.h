@@ -98,6 +98,6 @@ cudaError_t launch_cache_write(int d, bool bf16, bool e4m3, const CacheCopyParam
 cudaError_t launch_cache_read(int d, bool bf16, bool e4m3, const CacheCopyParams& p,
                               cudaStream_t stream);
 cudaError_t launch_tree(int d, bool bf16, bool e4m3, int rows, const CUtensorMap& tmk,
-                        const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream);
+                        const CUtensorMap& tmv, const TreeParams& p, int device, cudaStream_t stream);
 
 }  // namespace fa

@@ -329,7 +329,9 @@ extern "C" int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cac
   if (make_map_cache(&tmk, k_cache, p.c, d, p.box, format, dtype) != FA_OK ||
       make_map_cache(&tmv, v_cache, p.c, d, p.box, format, dtype) != FA_OK)
     return FA_ERR_CUDA;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return FA_ERR_CUDA;  // (< kMaxDevices, checked above)
   const cudaError_t e = launch_tree(d, dtype == FA_BF16, format == FA_CACHE_E4M3, rows, tmk, tmv, p,
-                                    static_cast<cudaStream_t>(stream));
+                                    device, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

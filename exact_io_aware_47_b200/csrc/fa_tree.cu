@@ -1472,17 +1472,23 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) fa_tree_join_kernel(const
 
 template <int D, bool BF16, bool E4M3, int R>
 static cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv, const TreeParams& p,
-                                 cudaStream_t stream) {
+                                 int device, cudaStream_t stream) {
   using Lay = TreeLayout<D, BF16, E4M3, R>;
   auto kern = fa_tree_kernel<D, BF16, E4M3, R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  if constexpr (R == 128) {
-    // the register split in the kernel assumes exactly this launch allocation
-    cudaFuncAttributes attr;
-    e = cudaFuncGetAttributes(&attr, kern);
+  // once per device: a decoding step is short
+  static std::atomic<unsigned long long> ready{0};
+  const unsigned long long bit = 1ull << device;
+  if ((ready.load(std::memory_order_relaxed) & bit) == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
     if (e != cudaSuccess) return e;
-    if (attr.numRegs != kTreeLaunchRegs) return cudaErrorInvalidConfiguration;
+    if constexpr (R == 128) {
+      // the register split in the kernel assumes exactly this launch allocation
+      cudaFuncAttributes attr;
+      e = cudaFuncGetAttributes(&attr, kern);
+      if (e != cudaSuccess) return e;
+      if (attr.numRegs != kTreeLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
+    ready.fetch_or(bit, std::memory_order_relaxed);
   }
   kern<<<p.grid, kTreeThreads, Lay::kSmemBytes, stream>>>(tmk, tmv, p);
   // items of one tile are never cut
@@ -1499,12 +1505,12 @@ static cudaError_t launch_tree_t(const CUtensorMap& tmk, const CUtensorMap& tmv,
 }
 
 cudaError_t launch_tree(int d, bool bf16, bool e4m3, int rows, const CUtensorMap& tmk,
-                        const CUtensorMap& tmv, const TreeParams& p, cudaStream_t stream) {
+                        const CUtensorMap& tmv, const TreeParams& p, int device, cudaStream_t stream) {
 #define FA_TREE_R(DD, BB, EE)                                                     \
-  (rows == 16   ? launch_tree_t<DD, BB, EE, 16>(tmk, tmv, p, stream)              \
-   : rows == 32 ? launch_tree_t<DD, BB, EE, 32>(tmk, tmv, p, stream)              \
-   : rows == 64 ? launch_tree_t<DD, BB, EE, 64>(tmk, tmv, p, stream)              \
-                : launch_tree_t<DD, BB, EE, 128>(tmk, tmv, p, stream))
+  (rows == 16   ? launch_tree_t<DD, BB, EE, 16>(tmk, tmv, p, device, stream)              \
+   : rows == 32 ? launch_tree_t<DD, BB, EE, 32>(tmk, tmv, p, device, stream)              \
+   : rows == 64 ? launch_tree_t<DD, BB, EE, 64>(tmk, tmv, p, device, stream)              \
+                : launch_tree_t<DD, BB, EE, 128>(tmk, tmv, p, device, stream))
   if (d == 128) {
     if (bf16) return e4m3 ? FA_TREE_R(128, true, true) : FA_TREE_R(128, true, false);
     return e4m3 ? FA_TREE_R(128, false, true) : FA_TREE_R(128, false, false);

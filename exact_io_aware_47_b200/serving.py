@@ -20,6 +20,7 @@ One decoding step::
 """
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -28,6 +29,7 @@ from . import _lib
 from .attention import _DTYPES, _E4M3, _check_inputs, _on_device
 
 _I64x3 = ctypes.c_int64 * 3
+_functions = {}      # the library's functions by name
 
 
 def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_len=None,
@@ -121,13 +123,15 @@ def _int32_arg(name, x, shape, device, other=None):
 
 
 def _launch(name, device, *args):
-    fn = getattr(_lib.load(), name)
-    stream = torch._C._cuda_getCurrentRawStream(device.index) or None
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index) or None)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index) or None)
     if status:
         _lib.check(name, status)
 
@@ -138,30 +142,38 @@ def _rope(name, q, k, inv_freq, positions, interleaved, factor, q_out, k_out):
         q, k, q_out, k_out = (None if t is None else t.unsqueeze(0) for t in (q, k, q_out, k_out))
     if q.dim() != 4:
         raise ValueError("q must be [B, H, N, d] or packed [H, T, d]")
-    B, Hq, N, d = q.shape
-    dev = q.device
-    if q.dtype not in _DTYPES:
+    shape = q.shape
+    B, Hq, N, d = shape
+    dev, dt = q.device, q.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
         raise ValueError("dtype must be bfloat16 or float16")
-    dt = q.dtype
-    shape = (B, Hq, N, d)
-    _check_strided("q", q, shape, dt, dev)
+    q_contiguous = q.is_contiguous()
+    if not (q.is_cuda and (q_contiguous or q.stride(-1) == 1)):
+        _check_strided("q", q, shape, dt, dev)
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = torch.empty_like(q) if q_contiguous else torch.empty(shape, dtype=dt, device=dev)
+        q_out_strides = None
     else:
         _check_strided("q_out", q_out, shape, dt, dev)
+        q_out_strides = _strides(q_out)
     Hk = 0
-    k_strides = k_out_strides = None
+    k_ptr = k_out_ptr = k_strides = k_out_strides = None
     if k is not None:
         if not torch.is_tensor(k) or k.dim() != 4:
             raise ValueError("k must have as many dimensions as q")
         Hk = k.shape[1]
         shape = (B, Hk, N, d)
         _check_strided("k", k, shape, dt, dev)
+        k_contiguous = k.is_contiguous()
         if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            k_out = torch.empty_like(k) if k_contiguous else torch.empty(shape, dtype=dt, device=dev)
         else:
             _check_strided("k_out", k_out, shape, dt, dev)
-        k_strides, k_out_strides = _strides(k), _strides(k_out)
+            k_out_strides = _strides(k_out)
+        if not k_contiguous:
+            k_strides = _strides(k)
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
     f = inv_freq
@@ -169,13 +181,13 @@ def _rope(name, q, k, inv_freq, positions, interleaved, factor, q_out, k_out):
             and f.is_contiguous()):
         _on_device("inv_freq", inv_freq, dev)
         f = torch.as_tensor(f, dtype=torch.float64).to(dev).contiguous()
-    if f.dim() != 1:
+    if len(f.shape) != 1:
         raise ValueError("inv_freq must be [rot / 2]")
     pos = _int32_arg("positions", positions, (N,), dev, (B, N))
-    _launch(name, dev, q.data_ptr(), _strides(q), q_out.data_ptr(), _strides(q_out), Hq, _ptr(k),
-            k_strides, _ptr(k_out), k_out_strides, Hk, _ptr(pos),
-            N if pos is not None and pos.dim() == 2 else 0, f.data_ptr(), B, N, d, 2 * f.numel(),
-            int(bool(interleaved)), float(factor), _DTYPES[dt])
+    _launch(name, dev, q.data_ptr(), None if q_contiguous else _strides(q), q_out.data_ptr(),
+            q_out_strides, Hq, k_ptr, k_strides, k_out_ptr, k_out_strides, Hk, _ptr(pos),
+            N if pos is not None and pos.dim() == 2 else 0, f.data_ptr(), B, N, d, 2 * f.shape[0],
+            1 if interleaved else 0, factor, code)
     if packed:
         q_out, k_out = q_out[0], None if k_out is None else k_out[0]
     return q_out, k_out
@@ -205,15 +217,17 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, B, device):
     """Checks a cache; returns (Hk, page, d, format, block_table, arguments)."""
     if not torch.is_tensor(k_cache) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, Hk, page_size, d]")
-    P, Hk, page, d = k_cache.shape
+    shape = k_cache.shape
+    P, Hk, page, d = shape
     dt = k_cache.dtype
     if dt not in _E4M3 and dt not in _DTYPES:
         raise ValueError("k_cache must be float8_e4m3fn (or uint8 codes), bfloat16 or float16")
-    _check("k_cache", k_cache, (P, Hk, page, d), dt, device)
-    _check("v_cache", v_cache, (P, Hk, page, d), dt, device)
+    _check("k_cache", k_cache, shape, dt, device)
+    _check("v_cache", v_cache, shape, dt, device)
     if dt in _E4M3:
-        _check("k_scale", k_scale, (P, Hk, page), torch.float32, device)
-        _check("v_scale", v_scale, (P, Hk, page), torch.float32, device)
+        shape = (P, Hk, page)
+        _check("k_scale", k_scale, shape, torch.float32, device)
+        _check("v_scale", v_scale, shape, torch.float32, device)
         fmt = _lib.FA_CACHE_E4M3
     else:
         if k_scale is not None or v_scale is not None:
@@ -298,6 +312,9 @@ def tree_workspace_bytes(B, Hq, Hk, T, d):
     return _lib.fa_fwd_tree_workspace_size(B, Hq, Hk, T, d)
 
 
+_tree_workspace_bytes = functools.lru_cache(maxsize=256)(tree_workspace_bytes)
+
+
 def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None, block_table=None,
                  k_scale=None, v_scale=None, scale=None, out=None, lse=None, workspace=None):
     """O, LSE of the drafted tokens q [B, Hq, T, d] (bf16/fp16) over a cache.
@@ -317,7 +334,8 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
     dev = q.device
     if q.dtype not in _DTYPES:
         raise ValueError("dtype must be bfloat16 or float16")
-    _check("q", q, (B, Hq, T, d), q.dtype, dev)
+    shape, dt = q.shape, q.dtype
+    _check("q", q, shape, dt, dev)
     Hk, page, dc, fmt, table, stride = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table,
                                                    B, dev)
     if dc != d:
@@ -333,7 +351,7 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
         if draft_lens is not None:
             lse.fill_(-math.inf)
-    _check("out", out, (B, Hq, T, d), q.dtype, dev)
+    _check("out", out, shape, dt, dev)
     _check("lse", lse, (B, Hq, T), torch.float32, dev)
     ctx = _int32_arg("ctx_lens", ctx_lens, (B,), dev)
     if ctx is None:
@@ -349,7 +367,7 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
         if mask.shape != (T, T) and mask.shape != (B, T, T):
             raise ValueError(f"tree_mask must be [{T}, {T}] or [{B}, {T}, {T}]")
     if workspace is None:
-        workspace = torch.empty(tree_workspace_bytes(B, Hq, Hk, T, d), dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(_tree_workspace_bytes(B, Hq, Hk, T, d), dtype=torch.uint8)
     _launch("fa_fwd_tree", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             _ptr(k_scale), _ptr(v_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _ptr(table), stride, ctx.data_ptr(),

@@ -572,7 +572,7 @@ def test_tree_wait_timeout_is_reported_and_the_context_stays_usable(fa, e4m3, T)
         _lib.fa_set_wait_limit_ns(prev)
     st, word = fa.device_status()
     assert st == _lib.FA_ERR_DEVICE_TIMEOUT, f"status {st} word {word:#x}"
-    assert (word >> 8) & 0xFF in range(61, 80), f"site of word {word:#x}"
+    assert (word >> 8) & 0xFF in range(60, 90), f"site of word {word:#x}"
     again, _ = c.run(fa)
     _ok(fa)
     assert torch.equal(good, again)
