@@ -66,52 +66,89 @@ __device__ __forceinline__ float row_amax(const uint4& v) {
   return max_nan(lo, hi);
 }
 
+// Slots of a thread's rows n1 + e kRows, -1 for those that are not copied: lane e
+// of a row's lanes looks up row e, the others are told.
+template <int D>
+__device__ __forceinline__ long long copy_slots(const CacheCopyParams& p, const CopyPart& c, int lane, int n1,
+                                                long long (&slot)[kCachePasses]) {
+  const int n = n1 + (lane & (kCachePasses - 1)) * CacheBlock<D>::kRows;
+  const long long mine = n < c.len ? cache_row(p.c, c.b, c.h, c.start + n) : -1;
+  if (lane < kCachePasses && n < c.len && mine < 0) record_error(kErrDeviceSeqlen, 4);
+#pragma unroll
+  for (int e = 0; e < kCachePasses; ++e)
+    slot[e] = __shfl_sync(0xffffffffu, mine, e, CacheBlock<D>::kLanes);
+  return mine;
+}
+
+// The copy is bound by its instructions, not by memory, unless what a row needs
+// once is done once: its slot, and the two divisions of its scale, which the
+// lanes of a row share out over the 2 x kCachePasses rows that they hold (150
+// instructions a vector before, and 60 against 48 us for the 256 MB of a
+// padded batch's prompts).
 template <int D, bool BF16, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_write_kernel(const CacheCopyParams p) {
-  constexpr int kLanes = CacheBlock<D>::kLanes;
+  constexpr int kLanes = CacheBlock<D>::kLanes, kRows = CacheBlock<D>::kRows;
   const CopyPart c = copy_part<D>(p);
   if (c.n0 >= c.len) return;
   const int lane = threadIdx.x % kLanes, n1 = c.n0 + threadIdx.x / kLanes;
-  const uint8_t* k = p.k + 2 * (c.b * p.ks.b + c.h * p.ks.h) + 16 * lane;
-  const uint8_t* v = p.v + 2 * (c.b * p.vs.b + c.h * p.vs.h) + 16 * lane;
+  const uint8_t* k = p.k + 2 * (c.b * p.ks.b + c.h * p.ks.h + n1 * p.ks.n) + 16 * lane;
+  const uint8_t* v = p.v + 2 * (c.b * p.vs.b + c.h * p.vs.h + n1 * p.vs.n) + 16 * lane;
+  const long long k_step = 2 * kRows * p.ks.n, v_step = 2 * kRows * p.vs.n;
   uint4 x[kCachePasses][2];
-  long long slot[kCachePasses];
 #pragma unroll
   for (int e = 0; e < kCachePasses; ++e) {
-    const int n = n1 + e * CacheBlock<D>::kRows;
     x[e][0] = x[e][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (n < c.len) {
-      x[e][0] = __ldcs(reinterpret_cast<const uint4*>(k + 2 * (n * p.ks.n)));
-      x[e][1] = __ldcs(reinterpret_cast<const uint4*>(v + 2 * (n * p.vs.n)));
+    if (n1 + e * kRows < c.len) {
+      x[e][0] = __ldcs(reinterpret_cast<const uint4*>(k + e * k_step));
+      x[e][1] = __ldcs(reinterpret_cast<const uint4*>(v + e * v_step));
     }
   }
+  long long slot[kCachePasses];
+  const long long mine = copy_slots<D>(p, c, lane, n1, slot);
+  if constexpr (E4M3) {
+    // lane l takes row l % 8 of the 8 (pass e, K or V: e = row / 2, w = row % 2);
+    // with 16 lanes the first 8 form 448 / top, the others top / 448
+    static_assert(2 * kCachePasses == 8, "8 rows for 8 or 16 lanes");
+    const int row = lane & 7;
+    float amax = 0.f;
 #pragma unroll
-  for (int e = 0; e < kCachePasses; ++e) {
-    const int n = n1 + e * CacheBlock<D>::kRows;
-    slot[e] = n < c.len ? cache_row(p.c, c.b, c.h, c.start + n) : -1;
-    if (n < c.len && slot[e] < 0 && lane == 0) record_error(kErrDeviceSeqlen, 4);
-  }
+    for (int e = 0; e < kCachePasses; ++e)
 #pragma unroll
-  for (int e = 0; e < kCachePasses; ++e) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint8_t* cache = w ? p.c.v : p.c.k;
-      if constexpr (E4M3) {
-        const float amax = row_amax<kLanes, BF16>(x[e][w]);  // whole warps: no lane has left
-        if (slot[e] < 0) continue;
-        const float top = fmaxf(amax, 448.f * 0x1p-126f);
-        float scale = amax > 0.f ? __fdiv_rn(top, 448.f) : 1.f;
-        if (!(amax < INFINITY)) {
-          scale = __int_as_float(0x7fffffff);  // the row reads back as NaN
-          if (lane == 0) record_error(kErrDeviceScale, 5);
-        }
-        reinterpret_cast<uint2*>(cache + slot[e] * D)[lane] =
-            to_e4m3x8(x[e][w], BF16, __fdiv_rn(448.f, top));
-        if (lane == 0) (w ? p.c.v_scale : p.c.k_scale)[slot[e]] = scale;
-      } else {
-        if (slot[e] >= 0) reinterpret_cast<uint4*>(cache + slot[e] * D * 2)[lane] = x[e][w];
+      for (int w = 0; w < 2; ++w) {
+        const float m = row_amax<kLanes, BF16>(x[e][w]);
+        if (row == 2 * e + w) amax = m;
       }
+    const long long at = __shfl_sync(0xffffffffu, mine, row >> 1, kLanes);
+    const float top = fmaxf(amax, 448.f * 0x1p-126f);
+    float inv, scale;
+    if constexpr (kLanes == 16) {
+      inv = scale = __fdiv_rn(lane < 8 ? 448.f : top, lane < 8 ? top : 448.f);
+    } else {
+      inv = __fdiv_rn(448.f, top);
+      scale = __fdiv_rn(top, 448.f);
     }
+    if (lane >= kLanes - 8 && at >= 0) {
+      if (!(amax > 0.f)) scale = 1.f;
+      if (!(amax < INFINITY)) {
+        scale = __int_as_float(0x7fffffff);  // the row reads back as NaN
+        record_error(kErrDeviceScale, 5);
+      }
+      ((row & 1) ? p.c.v_scale : p.c.k_scale)[at] = scale;
+    }
+#pragma unroll
+    for (int e = 0; e < kCachePasses; ++e)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const float f = __shfl_sync(0xffffffffu, inv, 2 * e + w, kLanes);
+        if (slot[e] >= 0)
+          reinterpret_cast<uint2*>((w ? p.c.v : p.c.k) + slot[e] * D)[lane] = to_e4m3x8(x[e][w], BF16, f);
+      }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kCachePasses; ++e)
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (slot[e] >= 0) reinterpret_cast<uint4*>((w ? p.c.v : p.c.k) + slot[e] * D * 2)[lane] = x[e][w];
   }
 }
 
@@ -139,12 +176,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
   if (c.n0 >= c.len) return;
   const int lane = threadIdx.x % kLanes, n1 = c.n0 + threadIdx.x / kLanes;
   long long slot[kCachePasses];
-#pragma unroll
-  for (int e = 0; e < kCachePasses; ++e) {
-    const int n = n1 + e * CacheBlock<D>::kRows;
-    slot[e] = n < c.len ? cache_row(p.c, c.b, c.h, c.start + n) : -1;
-    if (n < c.len && slot[e] < 0 && lane == 0) record_error(kErrDeviceSeqlen, 4);
-  }
+  copy_slots<D>(p, c, lane, n1, slot);
   using Vec = std::conditional_t<E4M3, uint2, uint4>;
   Vec x[kCachePasses][2];
   float scale[kCachePasses][2];
