@@ -47,7 +47,8 @@
 // (see below, at the rings).
 //
 // Work split.  All key tiles of all items form one line that is cut evenly
-// into one piece per CTA, whatever the lengths; an item that is cut leaves
+// into one piece per CTA, whatever the lengths (counting a few tiles for what
+// an item costs beside its keys); an item that is cut leaves
 // partial results (unnormalised O, r, sum) in the workspace, and
 // fa_tree_join_kernel adds them up in order.
 #include "fa_serve.h"
@@ -60,6 +61,11 @@ constexpr int kTreeThreads = 512;
 // 184, the other two keep 72 (2 x 184 + 2 x 72 = 4 x 128).
 constexpr int kTreeLaunchRegs = 128, kTreeSoftmaxRegs = 184, kTreeOtherRegs = 72;
 static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, "register split");
+// What an item's start and end cost, in tiles, where the line of work is cut.
+// Cuts at 0, 2, 4, 7: 64 sequences of 820..8192 keys, one row tile of 16, 133, 118,
+// 114, 112 us; of 200..2000 keys 73, 54, 48, 48 us; 16 sequences, 128 rows, 159, 131,
+// 123, 127 us.
+constexpr int kTreeItemCost = 4;
 constexpr float kTreeMinScale = 0x1p-90f;  // V scales below count as this (keeps sums in range)
 
 template <int D_, bool BF16, bool E4M3, int R_>
@@ -140,10 +146,13 @@ __device__ __forceinline__ int tree_tiles(const TreeLens& l) {
   return l.drafts > 0 ? static_cast<int>((static_cast<long long>(l.ctx) + l.drafts + 127) / 128) : 0;
 }
 
-// This CTA's walk over its piece of the line of key tiles, item by item.
+// This CTA's walk over its piece of the line, item by item.  An item takes
+// `cost` units (its start and end) and then one per key tile.
 struct TreeWalk {
-  int b, hk, rt, tile, nt;  // next item of sequence b (nt tiles each), first tile in it
-  int left;                 // tiles left in the piece
+  int b, hk, rt, nt;        // next item of sequence b (nt tiles each)
+  int unit;                 // where in it this CTA begins
+  int left;                 // units left in the piece
+  int cost;
   int ctx, drafts;
 };
 struct TreeSeg {
@@ -163,13 +172,17 @@ __device__ __forceinline__ bool tree_next(TreeWalk& w, const TreeParams& p, Tree
   s.b = w.b;
   s.hk = w.hk;
   s.rt = w.rt;
-  s.t0 = w.tile;
-  s.t1 = min(w.nt, w.tile + w.left);
+  s.t0 = max(0, w.unit - w.cost);
+  s.t1 = min(w.nt, w.unit - w.cost + w.left);
   s.nt = w.nt;
   s.ctx = w.ctx;
   s.drafts = w.drafts;
-  w.left -= s.t1 - s.t0;
-  w.tile = 0;
+  if (s.t1 <= s.t0) {  // (the piece ends within the item's cost)
+    w.left = 0;
+    return false;
+  }
+  w.left -= w.cost + w.nt - w.unit;
+  w.unit = 0;
   if (++w.rt == p.row_tiles) {
     w.rt = 0;
     ++w.hk;
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   TreeWalk* s_walk = reinterpret_cast<TreeWalk*>(const_cast<int*>(s_fix + 16));
   long long* s_scan = reinterpret_cast<long long*>(smem + Lay::kStat);  // setup only, one per warp
   static_assert(8 * (2 * kSlots + 16 + 14) + 4 * 18 + sizeof(TreeWalk) <= Lay::kBarBytes, "barrier area");
-  static_assert(Lay::kStatBytes >= kTreeThreads / 32 * 8, "scan scratch");
+  static_assert(Lay::kStatBytes >= kTreeThreads / 32 * 16, "scan scratch");
   const WaitCtl wc{abort_flag, p.wait_ns};
 
   const int warp = threadIdx.x >> 5;
@@ -518,26 +531,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int per = (p.B + kTreeThreads - 1) / kTreeThreads;
     const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
     const int items = p.c.Hk * p.row_tiles;
-    long long sum = 0;
+    long long tiles = 0, count = 0;              // of this thread's sequences
     for (int b = b0; b < b1; ++b) {
       const TreeLens l = tree_lens(p, b);
       if (l.bad && blockIdx.x == 0) record_error(kErrDeviceSeqlen, 60);
-      sum += static_cast<long long>(tree_tiles(l)) * items;
+      const int nt = tree_tiles(l);
+      tiles += static_cast<long long>(nt) * items;
+      count += nt > 0 ? items : 0;
     }
-    long long inc = sum;  // inclusive sum over the warp
+    long long it = tiles, ic = count;            // inclusive sums over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
+      const long long ut = __shfl_up_sync(0xffffffffu, it, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
+      if (lane >= o) {
+        it += ut;
+        ic += uc;
+      }
     }
-    if (lane == 31) s_scan[warp] = inc;
+    if (lane == 31) {
+      s_scan[2 * warp] = it;
+      s_scan[2 * warp + 1] = ic;
+    }
     __syncthreads();
-    long long before = inc - sum, total = 0;
+    long long bt = it - tiles, bc = ic - count, total_t = 0, total_c = 0;
     for (int w = 0; w < kTreeThreads / 32; ++w) {
-      const long long x = s_scan[w];
-      if (w < warp) before += x;
-      total += x;
+      const long long x = s_scan[2 * w], y = s_scan[2 * w + 1];
+      if (w < warp) {
+        bt += x;
+        bc += y;
+      }
+      total_t += x;
+      total_c += y;
     }
+    // an item's start and end take about as long as kTreeItemCost tiles; where
+    // there is no more than a few tiles for a CTA, they are spread evenly instead
+    const int cost = total_t >= 4ll * gridDim.x ? kTreeItemCost : 0;
+    const long long total = total_t + cost * total_c, before = bt + cost * bc, sum = tiles + cost * count;
     const long long lo = total / gridDim.x, rest = total % gridDim.x;
     const long long c = blockIdx.x;
     const long long p0 = lo * c + min(c, rest), p1 = p0 + lo + (c < rest ? 1 : 0);
@@ -547,15 +576,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int b = b0; b < b1; ++b) {
         const TreeLens l = tree_lens(p, b);
         const int nt = tree_tiles(l);
-        const long long here = static_cast<long long>(nt) * items;
+        const long long here = nt > 0 ? static_cast<long long>(nt + cost) * items : 0;
         if (p0 < at + here) {
+          const int item = static_cast<int>((p0 - at) / (nt + cost));
           s_walk->b = b;
-          const int item = static_cast<int>((p0 - at) / nt);
           s_walk->hk = item / p.row_tiles;
           s_walk->rt = item % p.row_tiles;
-          s_walk->tile = static_cast<int>((p0 - at) % nt);
           s_walk->nt = nt;
+          s_walk->unit = static_cast<int>((p0 - at) % (nt + cost));
           s_walk->left = static_cast<int>(p1 - p0);
+          s_walk->cost = cost;
           s_walk->ctx = l.ctx;
           s_walk->drafts = l.drafts;
           break;
@@ -569,16 +599,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   TreeWalk walk = *s_walk;
-  const int n_tiles = walk.left;
   __syncthreads();  // s_scan's memory holds the statistics from here on
   // whether this CTA's first item was begun by an earlier CTA: the join reads it
   if (threadIdx.x == 0) {
-    int* head = p.heads + blockIdx.x * 4;
-    const bool cont = n_tiles > 0 && walk.tile > 0;
-    head[0] = cont ? walk.b : -1;
-    head[1] = cont ? walk.hk * p.row_tiles + walk.rt : -1;
-    head[2] = cont && walk.tile + n_tiles >= walk.nt;  // it ends here
-    head[3] = cont ? walk.drafts : 0;
+    TreeWalk first = walk;
+    TreeSeg seg;
+    const bool cont = tree_next(first, p, seg) && seg.t0 > 0;
+    *reinterpret_cast<int4*>(p.heads + blockIdx.x * 4) =
+        cont ? make_int4(seg.b, seg.hk * p.row_tiles + seg.rt, seg.t1 == seg.nt, seg.drafts)
+             : make_int4(-1, -1, 0, 0);
   }
 
   if (warp >= 8) {
@@ -666,7 +695,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------- S^T = K Q^T
-    if (lane == 0 && n_tiles > 0) {
+    if (lane == 0) {
       constexpr uint32_t kFormat = E4M3 ? 0u : (BF16 ? 1u : 0u);
       constexpr uint32_t kIdesc = (1u << 4) | (kFormat << 7) | (kFormat << 10) |
                                   (static_cast<uint32_t>(Lay::kSCols >> 3) << 17) | (8u << 24);
@@ -715,7 +744,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------------------------- O^T += V^T P^T
-    if (lane == 0 && n_tiles > 0) {
+    if (lane == 0) {
       // both operands MN-major; e4m3 caches: A is e4m3 and B e5m2 (format 1), or
       // both are fp16
       constexpr bool k8 = Lay::kTerms8;
