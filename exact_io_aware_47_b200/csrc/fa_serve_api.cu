@@ -311,6 +311,9 @@ extern "C" int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cac
   const long long rows_all = static_cast<long long>(p.group) * T;
   const int rows = tree_rows(rows_all);
   p.row_tiles = static_cast<int>((rows_all + rows - 1) / rows);
+  // (a CTA counts its piece of all key tiles in 32 bits)
+  const long long most = static_cast<long long>(B) * Hk * p.row_tiles * ((p.c.room + 127) / 128);
+  if (most >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   p.box_log2 = 7;
   while (page_size % (1 << p.box_log2) != 0) --p.box_log2;  // (page_size is a multiple of 16)
   p.box = 1 << p.box_log2;
@@ -321,8 +324,6 @@ extern "C" int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cac
   DeviceInfo di;
   st = current_device_info(&di);
   if (st != FA_OK) return st;
-  const long long most = static_cast<long long>(B) * Hk * p.row_tiles *
-                         ((static_cast<long long>(p.c.table_stride) * page_size + 127) / 128);
   p.grid = di.num_sms < kTreeMaxCtas ? di.num_sms : kTreeMaxCtas;
   if (most < p.grid) p.grid = static_cast<int>(most);
   CUtensorMap tmk, tmv;

@@ -71,6 +71,7 @@ constexpr float kTreeMinScale = 0x1p-90f;  // V scales below count as this (keep
 template <int D_, bool BF16, bool E4M3, int R_>
 struct TreeLayout {
   static constexpr int D = D_, R = R_;
+  static constexpr bool kE4M3 = E4M3;
   static constexpr bool kTurns = R <= 32;                   // the groups take turns at the tiles
   static constexpr int kCols = kTurns ? R : R / 2;          // columns of a softmax thread
   static constexpr int kTermsQ = E4M3 ? (BF16 ? 2 : 3) : 1;
@@ -94,6 +95,11 @@ struct TreeLayout {
   static constexpr int kQPanel = R * 128;
   static constexpr int kQBytes = kTermsQ * kPanels * kQPanel;
   static constexpr int kQBufs = R == 128 ? 1 : 2;
+  // With one buffer for Q, nothing goes on while it is cut into terms: the softmax
+  // warps do half of the rows at an item's start (16 sequences x 128 rows, keys of
+  // 820..8192: 122 -> 121 us; 32 x 128 rows, 200..2000: 100 -> 95 us)
+  static constexpr bool kQHelp = E4M3 && kQBufs == 1;
+  static constexpr int kQRows = kQHelp ? R / 2 : R;         // rows of the three Q warps
   static constexpr int kScales = E4M3 ? 8 : 0;              // ring of tile scales, 1 KB each
   static constexpr int kV16Bufs = kConvert ? 2 : 0;         // converted V tiles
   static constexpr int kV16Bytes = (D + 63) / 64 * 16384;
@@ -462,6 +468,83 @@ __device__ __noinline__ void tree_add_not_finite(const TreeParams& p, int b, int
   }
 }
 
+// Rows BEGIN .. END - 1 of an item's Q, by WARPS warps of which this is number
+// `worker`: loads a batch ahead, the first ones on construction; store() puts
+// the rows in place, with an 8-bit cache as e4m3 terms and a scale per row.
+template <class Lay, bool BF16, int WARPS, int BEGIN, int END>
+struct TreeQ {
+  static constexpr int kLanes = Lay::D / 8;      // lanes of a row, 8 values each
+  static constexpr int kRowsWarp = 32 / kLanes;
+  static constexpr int kIters = (END - BEGIN + WARPS * kRowsWarp - 1) / (WARPS * kRowsWarp);
+  static constexpr int kBatch = kIters < 4 ? kIters : 4;
+  const uint8_t* q;
+  int rows, first, l;                            // rows that exist, this lane's first, its part of a row
+  uint4 next[kBatch];
+
+  __device__ __forceinline__ uint4 load(int it) const {
+    const int r = first + it * WARPS * kRowsWarp;
+    return r < END && r < rows ? *(reinterpret_cast<const uint4*>(q + static_cast<long long>(r) * Lay::D * 2) + l)
+                               : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ TreeQ(const TreeParams& p, const TreeSeg& seg, int lane, int worker) {
+    const long long row0 = (static_cast<long long>(seg.b) * p.Hq + static_cast<long long>(seg.hk) * p.group) * p.T +
+                           static_cast<long long>(seg.rt) * Lay::R;
+    q = p.q + row0 * Lay::D * 2;
+    rows = p.group * p.T - seg.rt * Lay::R;
+    first = BEGIN + worker * kRowsWarp + lane / kLanes;
+    l = lane % kLanes;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) next[k] = load(k);
+  }
+  __device__ __forceinline__ void store(uint8_t* qdst, float* qs, float scale_log2) {
+#pragma unroll 1
+    for (int it0 = 0; it0 < kIters; it0 += kBatch) {
+      uint4 xs[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        xs[k] = next[k];
+        next[k] = load(it0 + kBatch + k);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = first + (it0 + k) * WARPS * kRowsWarp;
+        const uint4 x = xs[k];
+        if constexpr (Lay::kE4M3) {
+          float f[8];
+          const float amax = row_amax<kLanes, BF16>(x);
+          unpack8<BF16>(x, f);
+          // up = 2^(7 - e), e the exponent of amax: amax up in [128, 256); the
+          // scaled row is exact in fp16 (down to its steps of 2^-24)
+          const int e = amax > 0.f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23), 8), 253) : 134;
+          const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
+          if (l == 0 && r < END) qs[r] = amax < INFINITY ? down * scale_log2 : __int_as_float(0x7fffffff);
+          uint32_t h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(f[2 * i] * up, f[2 * i + 1] * up);
+#pragma unroll
+          for (int t = 0; t < Lay::kTermsQ; ++t) {
+            uint32_t w[4];                       // pairs of codes
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[i] = pack_e4m3x2_f16(h[i]);
+              if (t + 1 < Lay::kTermsQ) h[i] = hsub2_bits(h[i], unpack_e4m3x2_f16(w[i]));
+            }
+            // 8 bytes at column 8 l of row r: chunk l / 2, swizzled by the row
+            const uint32_t at = r * 128 + ((((l >> 1) ^ (r & 7)) << 4) | ((l & 1) << 3));
+            if (r < END)
+              *reinterpret_cast<uint2*>(qdst + t * Lay::kQPanel + at) =
+                  make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+          }
+        } else {
+          const uint32_t at = (l >> 3) * Lay::kQPanel + r * 128 + (((l & 7) ^ (r & 7)) << 4);
+          if (r < END) *reinterpret_cast<uint4*>(qdst + at) = x;
+        }
+      }
+    }
+  }
+};
+
 template <int D, bool BF16, bool E4M3, int R>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -513,7 +596,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&p_full[s], Lay::kTurns ? 4 : 8);
       mbar_init(&s_free[s], Lay::kTurns ? 4 : 8);
-      mbar_init(&q_full[s], 3);
+      mbar_init(&q_full[s], Lay::kQHelp ? 3 + 8 : 3);
       mbar_init(&q_empty[s], 8);
       mbar_init(&v16_full[s], 3);
       mbar_init(&v16_empty[s], 1);
@@ -564,8 +647,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       total_c += y;
     }
     // an item's start and end take about as long as kTreeItemCost tiles; where
-    // there is no more than a few tiles for a CTA, they are spread evenly instead
-    const int cost = total_t >= 4ll * gridDim.x ? kTreeItemCost : 0;
+    // there are fewer than two tiles for a CTA, they are spread evenly instead
+    // (256 tiles: 15.8 us, with the cost 16.3; 512 tiles: 19.0, with it 16.8)
+    const int cost = total_t >= 2ll * gridDim.x ? kTreeItemCost : 0;
     const long long total = total_t + cost * total_c, before = bt + cost * bc, sum = tiles + cost * count;
     const long long lo = total / gridDim.x, rest = total % gridDim.x;
     const long long c = blockIdx.x;
@@ -787,12 +871,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------- Q
-    constexpr int kLanes = D / 8;                // lanes of a row, 8 values each
-    constexpr int kRowsWarp = 32 / kLanes;
-    const int rows_all = p.group * p.T;
-    constexpr int kIters = (R + 3 * kRowsWarp - 1) / (3 * kRowsWarp);  // of 3 warps x kRowsWarp rows
-    constexpr int kBatch = kIters < 4 ? kIters : 4;
-    const int sub = lane / kLanes, l = lane % kLanes;
     bool ok = true;
     TreeWalk walk_q = walk;
     int si = 0;                                  // items whose Q is prepared
@@ -800,68 +878,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       TreeSeg seg;
       if (!tree_next(walk_q, p, seg)) return false;
       const int qb = si % Lay::kQBufs;
-      const long long row0 = (static_cast<long long>(seg.b) * p.Hq + static_cast<long long>(seg.hk) * p.group) * p.T +
-                             static_cast<long long>(seg.rt) * R;
-      uint8_t* qdst = smem + Lay::kQ + qb * Lay::kQBytes;
-      // a batch of loads ahead of the rows that are worked at, the first ones
-      // before the buffer is free
-      auto load = [&](int it) {
-        const int r = (it * 3 + warp - 13) * kRowsWarp + sub;
-        return r < R && seg.rt * R + r < rows_all
-                   ? *(reinterpret_cast<const uint4*>(p.q + (row0 + r) * D * 2) + l)
-                   : make_uint4(0u, 0u, 0u, 0u);
-      };
-      uint4 next[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) next[k] = load(k);
+      // (the first loads are issued before the buffer is free)
+      TreeQ<Lay, BF16, 3, 0, Lay::kQRows> rows(p, seg, lane, warp - 13);
       ok = mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 69);
       if (!ok) return false;
-#pragma unroll 1
-      for (int it0 = 0; it0 < kIters; it0 += kBatch) {
-        uint4 xs[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          xs[k] = next[k];
-          next[k] = load(it0 + kBatch + k);
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-        const int r = ((it0 + k) * 3 + warp - 13) * kRowsWarp + sub;
-        const uint4 x = xs[k];
-        if constexpr (E4M3) {
-          float f[8];
-          const float amax = row_amax<kLanes, BF16>(x);
-          unpack8<BF16>(x, f);
-          // up = 2^(7 - e), e the exponent of amax: amax up in [128, 256); the
-          // scaled row is exact in fp16 (down to its steps of 2^-24)
-          const int e = amax > 0.f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23), 8), 253) : 134;
-          const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
-          if (l == 0 && r < R)
-            s_qs[qb * R + r] = amax < INFINITY ? down * p.scale_log2 : __int_as_float(0x7fffffff);
-          uint32_t h[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(f[2 * i] * up, f[2 * i + 1] * up);
-#pragma unroll
-          for (int t = 0; t < Lay::kTermsQ; ++t) {
-            uint32_t w[4];                       // pairs of codes
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              w[i] = pack_e4m3x2_f16(h[i]);
-              if (t + 1 < Lay::kTermsQ) h[i] = hsub2_bits(h[i], unpack_e4m3x2_f16(w[i]));
-            }
-            // 8 bytes at column 8 l of row r: chunk l / 2, swizzled by the row
-            const uint32_t at = r * 128 + ((((l >> 1) ^ (r & 7)) << 4) | ((l & 1) << 3));
-            if (r < R)
-              *reinterpret_cast<uint2*>(qdst + t * Lay::kQPanel + at) =
-                  make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-          }
-        } else {
-          const uint32_t at = (l >> 3) * Lay::kQPanel + r * 128 + (((l & 7) ^ (r & 7)) << 4);
-          if (r < R) *reinterpret_cast<uint4*>(qdst + at) = x;
-        }
-        }
-      }
+      rows.store(smem + Lay::kQ + qb * Lay::kQBytes, s_qs + qb * R, p.scale_log2);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
@@ -987,6 +1008,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const float* qs = s_qs + qb * R + col0;
       const int L = seg.ctx + seg.drafts;
       const int m0 = seg.rt * R + col0;          // first row of this thread's columns
+      if constexpr (Lay::kQHelp) {
+        // (the item before is behind both groups and its products: Q's buffer is free)
+        TreeQ<Lay, BF16, 8, Lay::kQRows, R> rows(p, seg, lane, warp);
+        rows.store(smem + Lay::kQ, s_qs, p.scale_log2);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[0]);
+      }
       ok = mbar_wait_warp(&q_full[qb], (si / Lay::kQBufs) & 1, wc, 70) && ok;
       if (tid < kCols) nr[tid] = 0.f;
       bool unset = true;                         // tid < kCols: column tid has no reference yet

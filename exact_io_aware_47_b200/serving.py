@@ -68,6 +68,8 @@ def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_len=N
         if original_len is None:
             raise ValueError("scaling 'ramp' needs original_len")
         low, high = ramp
+        if not low < high:
+            raise ValueError("ramp must be (low, high) with low < high")
         g = ((original_len * f / (2.0 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
         f = f * (g + (1.0 - g) / factor)
         out_factor = 1.0 + 0.1 * math.log(factor)
@@ -284,6 +286,8 @@ def cache_read(k_cache, v_cache, start, n, lens=None, block_table=None, k_scale=
     are left as they were in k_out, v_out, and are zero in new tensors."""
     if not torch.is_tensor(k_cache):
         raise ValueError("k_cache must be a CUDA tensor")
+    if start is None:
+        raise ValueError("start must be a tensor or a list [B]")
     dev = k_cache.device
     B = len(start)
     Hk, page, d, fmt, table, stride = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table,
@@ -363,11 +367,16 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
         if not (torch.is_tensor(mask) and mask.is_cuda and mask.device == dev
                 and mask.dtype in (torch.uint8, torch.bool) and mask.is_contiguous()):
             _on_device("tree_mask", tree_mask, dev)
+            if torch.as_tensor(mask).is_floating_point():  # (0 and -inf would mean the opposite)
+                raise ValueError("tree_mask must be uint8 or bool: nonzero where a query sees a key")
             mask = (torch.as_tensor(mask) != 0).to(dev).contiguous()
         if mask.shape != (T, T) and mask.shape != (B, T, T):
             raise ValueError(f"tree_mask must be [{T}, {T}] or [{B}, {T}, {T}]")
     if workspace is None:
         workspace = q.new_empty(_tree_workspace_bytes(B, Hq, Hk, T, d), dtype=torch.uint8)
+    elif not (torch.is_tensor(workspace) and workspace.is_cuda and workspace.device == dev
+              and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
     _launch("fa_fwd_tree", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             _ptr(k_scale), _ptr(v_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _ptr(table), stride, ctx.data_ptr(),

@@ -410,7 +410,8 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale
  *     aligned; its contents on entry do not matter.  Calls that may overlap on
  *     the GPU need one each.
  *   Results do not depend on the order in which the GPU runs the work.
- *   B*Hq*T*d < 2^31, B*Hk*ceil(Hq/Hk*T / 16) < 2^31; d in {64, 128}.
+ *   B*Hq*T*d < 2^31; B*Hk*ceil(Hq/Hk*T / 16)*ceil(positions of a table row /
+ *   128) < 2^31 (sufficient; more rows take larger tiles); d in {64, 128}.
  */
 size_t fa_fwd_tree_workspace_size(int B, int Hq, int Hk, int T, int d);
 int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

@@ -419,19 +419,15 @@ def test_tree_lengths_differ_widely(fa, e4m3):
     assert torch.equal(o, o3) and torch.equal(lse, lse3)
 
 
-@pytest.mark.parametrize("e4m3", [True, False])
-@pytest.mark.parametrize("dtype,d", [(BF16, 128), (FP16, 64), (FP16, 128)])
-@pytest.mark.parametrize("T", [1, 7, 13, 30])
-def test_tree_many_tiles_in_a_row(fa, dtype, d, e4m3, T):
-    """Enough keys that every SM works through tens of tiles and several items
-    (all rings go round many times), against float64 on the GPU."""
-    B, Hk, group, page = 14, 8, 4, 48
+def _random_batch(fa, dtype, d, e4m3, T, B, Hk, longest):
+    """Contexts of 0 .. longest - 1 positions, against float64 on the GPU."""
+    group, page = 4, 48
     g = torch.Generator(device="cuda").manual_seed(T + d)
-    ctx = torch.randint(1, 7000, (B,), generator=g, device="cuda").to(torch.int32)
-    per = (7000 + T + page - 1) // page
+    ctx = torch.randint(0 if longest < 1000 else 1, longest, (B,), generator=g, device="cuda").to(torch.int32)
+    per = (longest + T + page - 1) // page
     table = torch.randperm(B * per, generator=g, device="cuda").view(B, per).to(torch.int32)
     kc, vc, ks, vs = _pool(B * per, Hk, page, d, dtype, e4m3)
-    n = 7000 + T
+    n = longest + T
     k, v = (torch.randn(B, Hk, n, d, generator=g, device="cuda").to(dtype) for _ in range(2))
     fa.cache_write(k, v, kc, vc, lens=ctx + T, block_table=table, k_scale=ks, v_scale=vs)
     q = torch.randn(B, Hk * group, T, d, generator=g, device="cuda").to(dtype)
@@ -466,6 +462,24 @@ def test_tree_many_tiles_in_a_row(fa, dtype, d, e4m3, T):
         assert bool((err <= tol).all()), f"b{b} L{L}: worst {(err - tol).max().item():.3e}"
         lerr = (lse[b].double().view(Hk, group * T) - rl).abs()
         assert bool((lerr <= 2 * e + L * 2.0 ** -23 + 2.0 ** -22 * rl.abs()).all()), f"b{b}: LSE {lerr.max().item():.3e}"
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (FP16, 64), (FP16, 128)])
+@pytest.mark.parametrize("T", [1, 7, 13, 30])
+def test_tree_many_tiles_in_a_row(fa, dtype, d, e4m3, T):
+    """Enough keys that every SM works through tens of tiles and several items
+    (all rings go round many times)."""
+    _random_batch(fa, dtype, d, e4m3, T, 14, 8, 7000)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (FP16, 64)])
+@pytest.mark.parametrize("T", [1, 5, 16, 20])
+def test_tree_many_short_items(fa, dtype, d, e4m3, T):
+    """Items of one to four tiles, several per SM: pieces of the work begin and
+    end in what an item counts beside its keys."""
+    _random_batch(fa, dtype, d, e4m3, T, 150, 4, 400)
 
 
 @pytest.mark.parametrize("dtype,e4m3", [(BF16, True), (FP16, True), (BF16, False)])
@@ -536,6 +550,29 @@ def test_tree_masked_keys_may_hold_anything(fa, bad, e4m3):
             assert torch.equal(rest, clean[0, :, 1, [c for c in range(d) if c != 5]])
         if bad != "lowest" and math.isnan(value):
             assert torch.isnan(o[0, :, 1]).any()
+
+
+def test_tree_refuses_masks_and_workspaces_that_it_cannot_use(fa):
+    """A mask of additive terms means the opposite of one of flags, and a
+    workspace elsewhere would be written to; nothing is launched for either."""
+    c = Tree(B=2, Hq=2, Hk=1, T=2, ctx=(30, 30), d=64, page=16, dtype=BF16, seed=16)
+    good, _ = c.run(fa)
+
+    def run(**kw):
+        return fa.forward_tree(c.q, c.kc, c.vc, torch.tensor([30, 30], dtype=torch.int32).cuda(),
+                               k_scale=c.ks, v_scale=c.vs, block_table=c.table.cuda(), **kw)[0]
+    flags = torch.as_tensor(c.mask).cuda()
+    need = fa.tree_workspace_bytes(2, 2, 1, 2, 64)
+    for bad in (flags.float(), torch.zeros(2, 2), [[0.0, -math.inf], [0.0, 0.0]]):
+        with pytest.raises(ValueError):
+            run(tree_mask=bad)
+    for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8).cuda()[::2],
+                need):
+        with pytest.raises(ValueError):
+            run(tree_mask=flags, workspace=bad)
+    o = run(tree_mask=flags, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    _ok(fa)
+    assert torch.equal(o, good)
 
 
 def test_tree_reports_bad_lengths_and_pages(fa):

@@ -117,7 +117,8 @@ def test_rope_frequencies():
     assert np.allclose(g.numpy()[mid], _freq(64)[mid] * (part + (1 - part) / 4), rtol=1e-14)
     assert a == pytest.approx(1 + 0.1 * math.log(4))
     for bad in (dict(rot=7), dict(rot=64, factor=0.5), dict(rot=64, scaling="other"),
-                dict(rot=64, scaling="ramp", factor=2.0), dict(rot=64, factor=float("nan"))):
+                dict(rot=64, scaling="ramp", factor=2.0), dict(rot=64, factor=float("nan")),
+                dict(rot=64, scaling="ramp", factor=2.0, original_len=4096, ramp=(4.0, 4.0))):
         with pytest.raises(ValueError):
             rope_frequencies(**bad)
 
@@ -237,6 +238,8 @@ def test_tree_refusals(lib):
     assert tree(ctx=P + 2) == _lib.FA_ERR_ALIGNMENT and tree(drafts=P + 2) == _lib.FA_ERR_ALIGNMENT
     assert tree(w=None) == _lib.FA_ERR_WORKSPACE and tree(wb=ws - 1) == _lib.FA_ERR_WORKSPACE
     assert tree(w=P + 16) == _lib.FA_ERR_ALIGNMENT
+    # more key tiles than the kernel counts
+    assert tree(B=1 << 10, stride=1 << 20, page=1 << 12) == _lib.FA_ERR_UNSUPPORTED
     assert lib.fa_fwd_tree_workspace_size(2, 3, 2, 3, 64) == 0
     assert lib.fa_fwd_tree_workspace_size(2, 4, 2, 3, 80) == 0
 
@@ -262,3 +265,5 @@ def test_binding_refuses_what_the_library_cannot_see():
         fa.cache_read(cache, cache, [0, 0], 4)
     with pytest.raises(ValueError):
         fa.cache_read(None, cache, [0, 0], 4)
+    with pytest.raises(ValueError):
+        fa.cache_read(cache, cache, None, 4)
