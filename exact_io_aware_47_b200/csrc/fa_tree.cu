@@ -21,7 +21,7 @@
 //     2^11, so that small probabilities are not lost beside a large one): 3
 //     terms, rounded at the end (9 bits, finer than bf16), or all 4 (exact).
 //   With 64 rows and more, where the softmax's instructions and the products
-//   weigh more than the cache, P stays fp16 and three warps that have time
+//   weigh more than the cache, P stays fp16 and four warps that have time
 //   convert V to fp16 (exact; half the products and no terms to cut).
 // The scale of a K row multiplies its row of S^T, the scale of a V row its
 // row of P^T: both are one thread's.
@@ -37,9 +37,9 @@
 // tile costs with few rows is latency); from 64 rows on they share each tile,
 // half of the columns each (a thread holds its columns in registers).
 //
-// Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warps 8 and 9
-// load K and V (TMA), warp 12 the scales, warp 10 issues the products of S, warp
-// 11 those of O, warps 13-15 prepare Q (and convert V).
+// Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax, warp 8 loads K
+// and the scales, warp 9 V (TMA), warp 10 issues the products of S, warp 11 those
+// of O, warps 12-15 prepare Q (and convert V).
 // An issuing thread pays about 60 cycles for an MMA and 210 for a commit
 // (measured, whatever the size), so S and O have a thread each, and there is
 // one commit per product: the barrier that gives a K or V slot back to the
@@ -99,8 +99,8 @@ struct TreeLayout {
   // warps do half of the rows at an item's start (16 sequences x 128 rows, keys of
   // 820..8192: 122 -> 121 us; 32 x 128 rows, 200..2000: 100 -> 95 us)
   static constexpr bool kQHelp = E4M3 && kQBufs == 1;
-  static constexpr int kQRows = kQHelp ? R / 2 : R;         // rows of the three Q warps
-  static constexpr int kScales = E4M3 ? 8 : 0;              // ring of tile scales, 1 KB each
+  static constexpr int kQRows = kQHelp ? R / 2 : R;         // rows of the four Q warps
+  static constexpr int kScales = E4M3 ? 8 : 0;              // ring of tile scales, 1 KB each (see below)
   static constexpr int kV16Bufs = kConvert ? 2 : 0;         // converted V tiles
   static constexpr int kV16Bytes = (D + 63) / 64 * 16384;
   // per row: Q scales; per group and column: reference, its last change and
@@ -113,6 +113,7 @@ struct TreeLayout {
   static constexpr int kSlots = kSlotsFit < 12 ? kSlotsFit : 12;
   static constexpr int kSlotsK = kSlots / 2, kSlotsV = kSlots - kSlotsK;  // two rings
   static_assert(kSlotsK >= 2, "a slot is reused two tiles later at the earliest (see below)");
+  static_assert(!E4M3 || kScales >= kSlotsK + 2, "scales are read before they are overwritten (see below)");
   static constexpr int kV = kSlotsK * kSlotBytes;
   static constexpr int kV16 = kSlots * kSlotBytes;
   static constexpr int kP = kV16 + kV16Bufs * kV16Bytes;
@@ -203,7 +204,11 @@ __device__ __forceinline__ bool tree_next(TreeWalk& w, const TreeParams& p, Tree
 // its last tile.  No phase can be missed there: with n >= 2 slots the next one
 // of the same slot belongs to S(i + 2), O(i) or a later tile, whose product
 // waits for that very softmax step or, S(i + 2), for all warps to have read
-// S(i) (both issuing threads go in order).  Nor can
+// S(i) (both issuing threads go in order).  The scales of tile i come with K(i)
+// and are read once S(i) is complete, before S(i)'s columns are given back; tile
+// i + 8's overwrite them after S(i + 8 - n), which waited for that (with barriers
+// of their own the scales cost two more waits a tile: 112 against 106 us for 64
+// sequences of 820..8192 keys, 121 against 115 for 16 with 128 rows).  Nor can
 // a wait be early (a parity wait returns at once while the phase before is still
 // open): whoever waits for a round of a slot has waited for the round before, or
 // for what followed from it.
@@ -563,9 +568,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
   uint64_t* kv_full = bars;                     // [kSlots]: the K ring, the V ring
   uint64_t* kv_empty = kv_full + kSlots;        // [kSlots]
-  uint64_t* sc_full = kv_empty + kSlots;        // [8]
-  uint64_t* sc_empty = sc_full + 8;             // [8]
-  uint64_t* p_full = sc_empty + 8;              // [2]
+  uint64_t* p_full = kv_empty + kSlots;         // [2]
   uint64_t* s_free = p_full + 2;                // [2]
   uint64_t* q_full = s_free + 2;                // [2]
   uint64_t* q_empty = q_full + 2;               // [2]
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   volatile int* s_fix = abort_flag + 1;         // [4 items][4 warps or groups that look]
   TreeWalk* s_walk = reinterpret_cast<TreeWalk*>(const_cast<int*>(s_fix + 16));
   long long* s_scan = reinterpret_cast<long long*>(smem + Lay::kStat);  // setup only, one per warp
-  static_assert(8 * (2 * kSlots + 16 + 14) + 4 * 18 + sizeof(TreeWalk) <= Lay::kBarBytes, "barrier area");
+  static_assert(8 * (2 * kSlots + 14) + 4 * 18 + sizeof(TreeWalk) <= Lay::kBarBytes, "barrier area");
   static_assert(Lay::kStatBytes >= kTreeThreads / 32 * 16, "scan scratch");
   const WaitCtl wc{abort_flag, p.wait_ns};
 
@@ -587,18 +590,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], Lay::kConvert && s >= kSlotsK ? 3 : 1);
-    }
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(&sc_full[s], 1);
-      mbar_init(&sc_empty[s], Lay::kTurns ? 4 : 8);
+      mbar_init(&kv_empty[s], Lay::kConvert && s >= kSlotsK ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&p_full[s], Lay::kTurns ? 4 : 8);
       mbar_init(&s_free[s], Lay::kTurns ? 4 : 8);
-      mbar_init(&q_full[s], Lay::kQHelp ? 3 + 8 : 3);
+      mbar_init(&q_full[s], Lay::kQHelp ? 4 + 8 : 4);
       mbar_init(&q_empty[s], 8);
-      mbar_init(&v16_full[s], 3);
+      mbar_init(&v16_full[s], 4);
       mbar_init(&v16_empty[s], 1);
       mbar_init(&drain[s], 1);
     }
@@ -714,6 +713,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const TreeBatch cur = next;
       next = at.next(p, lane);
       int z = tree_place(p, cur);
+      // (a bad page takes the scales of page 0)
+      const long long row = static_cast<long long>(max(z, 0)) * p.c.page_size + cur.y;
       if (z < 0) {  // read as zeros, past the map's last slice
         z = p.c.num_pages * p.c.Hk;
         record_error(kErrDeviceSeqlen, 60);
@@ -723,13 +724,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (!ok) break;
         const int copies = TreeTiles::copies(p, cur, j), mine = TreeTiles::turn(p, j, lane);
         if (lane == 0)
-          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(copies * p.box * 128 * Lay::kPanels));
+          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(copies * p.box * (128 * Lay::kPanels +
+                                                                                     (E4M3 && !is_v ? 8 : 0))));
         __syncwarp();
         if (mine < copies) {
 #pragma unroll
           for (int pn = 0; pn < Lay::kPanels; ++pn)
             tma_load_3d(slots + slot * Lay::kSlotBytes + pn * 16384 + mine * p.box * 128, map,
                         &full[slot], pn * Lay::kPanelElems, cur.y, z);
+          if (E4M3 && !is_v) {                   // scales of both come with K
+            float* dst = reinterpret_cast<float*>(smem + Lay::kScale + loaded % Lay::kScales * 1024) + mine * p.box;
+            bulk_load(dst, p.c.k_scale + row, 4u * p.box, &full[slot]);
+            bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &full[slot]);
+          }
         }
         ++loaded;
         if (++slot == ring) {
@@ -742,41 +749,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int i = max(0, loaded - ring); i < loaded; ++i)
       mbar_wait_drain(&full[i % ring], (i / ring) & 1, 200000000ull);
     __syncwarp();
-  } else if (warp == 12) {
-    // ------------------------------------------------------------- scales
-    if constexpr (E4M3) {
-      TreeTiles at(walk);
-      TreeBatch next = at.next(p, lane);
-      int done = 0;
-      bool ok = true;
-      while (ok && next.tiles > 0) {
-        const TreeBatch cur = next;
-        next = at.next(p, lane);
-        // (a bad page, reported by the K and V warps, takes the scales of page 0)
-        const long long row = static_cast<long long>(max(tree_place(p, cur), 0)) * p.c.page_size + cur.y;
-        for (int j = 0; j < cur.tiles; ++j) {
-          const int ss = done % Lay::kScales;
-          ok = mbar_wait_warp(&sc_empty[ss], ((done / Lay::kScales) & 1) ^ 1, wc, 63);
-          if (!ok) break;
-          const int copies = TreeTiles::copies(p, cur, j), mine = TreeTiles::turn(p, j, lane);
-          if (lane == 0) mbar_arrive_expect_tx(&sc_full[ss], 8u * p.box * copies);
-          __syncwarp();
-          if (mine < copies) {
-            float* dst = reinterpret_cast<float*>(smem + Lay::kScale + ss * 1024) + mine * p.box;
-            bulk_load(dst, p.c.k_scale + row, 4u * p.box, &sc_full[ss]);
-            bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &sc_full[ss]);
-          }
-          ++done;
-        }
-      }
-      for (int s = 0; s < Lay::kScales; ++s) {
-        if (done > s) {
-          const int last = done - 1 - ((done - 1 - s) % Lay::kScales);
-          mbar_wait_drain(&sc_full[s], (last / Lay::kScales) & 1, 200000000ull);
-        }
-      }
-      __syncwarp();
-    }
   } else if (warp == 10) {
     // ------------------------------------------------------------- S^T = K Q^T
     if (lane == 0) {
@@ -879,7 +851,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!tree_next(walk_q, p, seg)) return false;
       const int qb = si % Lay::kQBufs;
       // (the first loads are issued before the buffer is free)
-      TreeQ<Lay, BF16, 3, 0, Lay::kQRows> rows(p, seg, lane, warp - 13);
+      TreeQ<Lay, BF16, 4, 0, Lay::kQRows> rows(p, seg, lane, warp - 12);
       ok = mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 69);
       if (!ok) return false;
       rows.store(smem + Lay::kQ + qb * Lay::kQBytes, s_qs + qb * R, p.scale_log2);
@@ -903,7 +875,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       int i = 0, slot = 0, round = 0;
       for (int item = 0; ok && tree_next(walk, p, seg); ++item) {
         const int L = seg.ctx + seg.drafts;
-        volatile int* fix = s_fix + (item & 3) * 4 + warp - 13;
+        volatile int* fix = s_fix + (item & 3) * 4 + warp - 12;
         if (lane == 0) *fix = 0;
         __syncwarp();
         for (int tile = seg.t0; tile < seg.t1; ++tile, ++i) {
@@ -916,7 +888,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           bool found = false;
           // a unit: 16 columns of 32 rows, a row per lane
 #pragma unroll 2
-          for (int unit = warp - 13; unit < 4 * (D / 16); unit += 3) {
+          for (int unit = warp - 12; unit < 4 * (D / 16); unit += 4) {
             const int row = (unit & 3) * 32 + lane, ch = unit >> 2, sw = row & 7;
             uint4 v = *reinterpret_cast<const uint4*>(from + row * 128 + ((ch ^ sw) << 4));
             if (edge) {
@@ -989,19 +961,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if constexpr (Lay::kConvert) return mbar_wait_warp(&v16_empty[i & 1], (i >> 1) & 1, wc, site);
       else return mbar_wait_warp(&kv_empty[kSlotsK + i % kSlotsV], (i / kSlotsV) & 1, wc, site);
     };
-    // scales of this thread's row in tile i, taken from the ring while the tile
-    // before is worked at
-    float sk = 1.f, sv = 1.f;
-    auto take_scales = [&](int i) {
-      const int ss = i % Lay::kScales;
-      const bool ready = mbar_wait_warp(&sc_full[ss], (i / Lay::kScales) & 1, wc, 71);
-      const float* sc = reinterpret_cast<const float*>(smem + Lay::kScale + ss * 1024);
-      sk = sc[tid];
-      sv = sc[128 + tid];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sc_empty[ss]);
-      return ready;
-    };
     TreeSeg seg;
     for (int si = 0; tree_next(walk, p, seg); ++si) {
       const int qb = si % Lay::kQBufs;
@@ -1037,7 +996,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool any = tile < seg.t1;            // this group has a tile of the item
       if (!any && lane == 0) mbar_arrive(&q_empty[qb]);
       int last = i;                              // its last one
-      bool scales_taken = false;
       for (; begun && tile < seg.t1; tile += kEvery, i += kEvery) {
         last = i;
         const int key = tile * 128 + tid;
@@ -1062,24 +1020,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         if (threadIdx.x == 0) FA_TRACE_AT(i, 0);
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 1);
+        ok = wait_s(i, 72) && ok;  // S(i) is complete, and so are the copies it was made from
+        if (threadIdx.x == 0) FA_TRACE_AT(i, 2);
+        tc_fence_after();
         // (rows past the sequence have no scales; a V scale that is not a size
         // makes its row's probabilities NaN)
         float sk_now = 1.f, sv_now = 1.f, lv = 0.f;
         if constexpr (E4M3) {
-          if (!scales_taken) ok = take_scales(i) && ok;
-          scales_taken = false;
           if (key < L) {
-            sk_now = sk;
-            sv_now = sv;
+            const float* sc = reinterpret_cast<const float*>(smem + Lay::kScale + i % Lay::kScales * 1024);
+            sk_now = sc[tid];
+            sv_now = sc[128 + tid];
             if (!(sv_now >= kTreeMinScale && sv_now < INFINITY))
               sv_now = sv_now >= 0.f && sv_now < 1.f ? kTreeMinScale : NAN;
           }
           lv = lg2_approx(sv_now);
         }
-        if (threadIdx.x == 0) FA_TRACE_AT(i, 1);
-        ok = wait_s(i, 72) && ok;  // S(i) is complete
-        if (threadIdx.x == 0) FA_TRACE_AT(i, 2);
-        tc_fence_after();
         // d: exponent of a probability against its row's reference (without
         // the V scale sv = 2^lv, which multiplies what is stored)
         float d[kCols];
@@ -1210,10 +1167,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         if (threadIdx.x == 0) FA_TRACE_AT(i, 4);
-        if (E4M3 && tile + kEvery < seg.t1) {
-          ok = take_scales(i + kEvery) && ok;
-          scales_taken = true;
-        }
         // the product that read this P buffer before is complete (so V(i - 2), and
         // with it the slot's round before V(i)'s, is known to have come and gone)
         if (i >= Lay::kPBufs) ok = wait_o(i - Lay::kPBufs, 75) && ok;
@@ -1364,7 +1317,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       named_bar_sync(bar_id, 128);
       const volatile int* found = s_fix + (si & 3) * 4;
-      const int fix = found[0] | found[1] | (Lay::kConvert ? found[2] : 0);
+      const int fix = found[0] | found[1] | (Lay::kConvert ? found[2] | found[3] : 0);
       constexpr int kOut = Lay::kTurns ? 8 : 16;  // columns at a time
 #pragma unroll 1
       for (int c = 0; c < R / 2; c += kOut) {
