@@ -58,8 +58,9 @@ namespace fa {
 constexpr int kTreeThreads = 512;
 // Registers: 512 threads are launched with 128 each.  With 128 rows a softmax
 // thread holds 64 columns (scores and sums) and needs more: its warpgroups take
-// 184, the other two keep 72 (2 x 184 + 2 x 72 = 4 x 128).
-constexpr int kTreeLaunchRegs = 128, kTreeSoftmaxRegs = 184, kTreeOtherRegs = 72;
+// 176, the other two keep 80 (2 x 176 + 2 x 80 = 4 x 128; 16 sequences with 128
+// rows: 109 us, with 184 and 72 111, with 192 and 64 112).
+constexpr int kTreeLaunchRegs = 128, kTreeSoftmaxRegs = 176, kTreeOtherRegs = 80;
 static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, "register split");
 // What an item's start and end cost, in tiles, where the line of work is cut.
 // Cuts at 0, 2, 4, 7: 64 sequences of 820..8192 keys, one row tile of 16, 133, 118,
@@ -95,11 +96,6 @@ struct TreeLayout {
   static constexpr int kQPanel = R * 128;
   static constexpr int kQBytes = kTermsQ * kPanels * kQPanel;
   static constexpr int kQBufs = R == 128 ? 1 : 2;
-  // With one buffer for Q, nothing goes on while it is cut into terms: the softmax
-  // warps do half of the rows at an item's start (16 sequences x 128 rows, keys of
-  // 820..8192: 122 -> 121 us; 32 x 128 rows, 200..2000: 100 -> 95 us)
-  static constexpr bool kQHelp = E4M3 && kQBufs == 1;
-  static constexpr int kQRows = kQHelp ? R / 2 : R;         // rows of the four Q warps
   static constexpr int kScales = E4M3 ? 8 : 0;              // ring of tile scales, 1 KB each (see below)
   static constexpr int kV16Bufs = kConvert ? 2 : 0;         // converted V tiles
   static constexpr int kV16Bytes = (D + 63) / 64 * 16384;
@@ -473,22 +469,22 @@ __device__ __noinline__ void tree_add_not_finite(const TreeParams& p, int b, int
   }
 }
 
-// Rows BEGIN .. END - 1 of an item's Q, by WARPS warps of which this is number
-// `worker`: loads a batch ahead, the first ones on construction; store() puts
+// An item's Q, by WARPS warps of which this is number `worker` (four do 128 rows in
+// the time of an item's end, 7000 cycles): loads a batch ahead, the first ones on construction; store() puts
 // the rows in place, with an 8-bit cache as e4m3 terms and a scale per row.
-template <class Lay, bool BF16, int WARPS, int BEGIN, int END>
+template <class Lay, bool BF16, int WARPS>
 struct TreeQ {
   static constexpr int kLanes = Lay::D / 8;      // lanes of a row, 8 values each
   static constexpr int kRowsWarp = 32 / kLanes;
-  static constexpr int kIters = (END - BEGIN + WARPS * kRowsWarp - 1) / (WARPS * kRowsWarp);
-  static constexpr int kBatch = kIters < 4 ? kIters : 4;
+  static constexpr int kPass = WARPS * kRowsWarp;  // rows of all warps at a time
+  static constexpr int kBatch = Lay::R < 4 * kPass ? (Lay::R + kPass - 1) / kPass : 4;
   const uint8_t* q;
   int rows, first, l;                            // rows that exist, this lane's first, its part of a row
   uint4 next[kBatch];
 
   __device__ __forceinline__ uint4 load(int it) const {
-    const int r = first + it * WARPS * kRowsWarp;
-    return r < END && r < rows ? *(reinterpret_cast<const uint4*>(q + static_cast<long long>(r) * Lay::D * 2) + l)
+    const int r = first + it * kPass;
+    return r < Lay::R && r < rows ? *(reinterpret_cast<const uint4*>(q + static_cast<long long>(r) * Lay::D * 2) + l)
                                : make_uint4(0u, 0u, 0u, 0u);
   }
   __device__ __forceinline__ TreeQ(const TreeParams& p, const TreeSeg& seg, int lane, int worker) {
@@ -496,14 +492,14 @@ struct TreeQ {
                            static_cast<long long>(seg.rt) * Lay::R;
     q = p.q + row0 * Lay::D * 2;
     rows = p.group * p.T - seg.rt * Lay::R;
-    first = BEGIN + worker * kRowsWarp + lane / kLanes;
+    first = worker * kRowsWarp + lane / kLanes;
     l = lane % kLanes;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) next[k] = load(k);
   }
   __device__ __forceinline__ void store(uint8_t* qdst, float* qs, float scale_log2) {
 #pragma unroll 1
-    for (int it0 = 0; it0 < kIters; it0 += kBatch) {
+    for (int it0 = 0; it0 * kPass < Lay::R; it0 += kBatch) {
       uint4 xs[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
@@ -512,7 +508,7 @@ struct TreeQ {
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int r = first + (it0 + k) * WARPS * kRowsWarp;
+        const int r = first + (it0 + k) * kPass;
         const uint4 x = xs[k];
         if constexpr (Lay::kE4M3) {
           float f[8];
@@ -523,7 +519,7 @@ struct TreeQ {
           const int e = amax > 0.f ? min(max(static_cast<int>(__float_as_uint(amax) >> 23), 8), 253) : 134;
           const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
           const float down = __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
-          if (l == 0 && r < END) qs[r] = amax < INFINITY ? down * scale_log2 : __int_as_float(0x7fffffff);
+          if (l == 0 && r < Lay::R) qs[r] = amax < INFINITY ? down * scale_log2 : __int_as_float(0x7fffffff);
           uint32_t h[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(f[2 * i] * up, f[2 * i + 1] * up);
@@ -537,13 +533,13 @@ struct TreeQ {
             }
             // 8 bytes at column 8 l of row r: chunk l / 2, swizzled by the row
             const uint32_t at = r * 128 + ((((l >> 1) ^ (r & 7)) << 4) | ((l & 1) << 3));
-            if (r < END)
+            if (r < Lay::R)
               *reinterpret_cast<uint2*>(qdst + t * Lay::kQPanel + at) =
                   make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
           }
         } else {
           const uint32_t at = (l >> 3) * Lay::kQPanel + r * 128 + (((l & 7) ^ (r & 7)) << 4);
-          if (r < END) *reinterpret_cast<uint4*>(qdst + at) = x;
+          if (r < Lay::R) *reinterpret_cast<uint4*>(qdst + at) = x;
         }
       }
     }
@@ -595,7 +591,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&p_full[s], Lay::kTurns ? 4 : 8);
       mbar_init(&s_free[s], Lay::kTurns ? 4 : 8);
-      mbar_init(&q_full[s], Lay::kQHelp ? 4 + 8 : 4);
+      mbar_init(&q_full[s], 4);
       mbar_init(&q_empty[s], 8);
       mbar_init(&v16_full[s], 4);
       mbar_init(&v16_empty[s], 1);
@@ -851,7 +847,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!tree_next(walk_q, p, seg)) return false;
       const int qb = si % Lay::kQBufs;
       // (the first loads are issued before the buffer is free)
-      TreeQ<Lay, BF16, 4, 0, Lay::kQRows> rows(p, seg, lane, warp - 12);
+      TreeQ<Lay, BF16, 4> rows(p, seg, lane, warp - 12);
       ok = mbar_wait_warp(&q_empty[qb], ((si / Lay::kQBufs) & 1) ^ 1, wc, 69);
       if (!ok) return false;
       rows.store(smem + Lay::kQ + qb * Lay::kQBytes, s_qs + qb * R, p.scale_log2);
@@ -967,14 +963,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const float* qs = s_qs + qb * R + col0;
       const int L = seg.ctx + seg.drafts;
       const int m0 = seg.rt * R + col0;          // first row of this thread's columns
-      if constexpr (Lay::kQHelp) {
-        // (the item before is behind both groups and its products: Q's buffer is free)
-        TreeQ<Lay, BF16, 8, Lay::kQRows, R> rows(p, seg, lane, warp);
-        rows.store(smem + Lay::kQ, s_qs, p.scale_log2);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[0]);
-      }
       ok = mbar_wait_warp(&q_full[qb], (si / Lay::kQBufs) & 1, wc, 70) && ok;
       if (tid < kCols) nr[tid] = 0.f;
       bool unset = true;                         // tid < kCols: column tid has no reference yet
