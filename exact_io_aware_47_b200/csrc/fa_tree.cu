@@ -25,6 +25,16 @@
 //   convert V to fp16 (exact; half the products and no terms to cut).
 // The scale of a K row multiplies its row of S^T, the scale of a V row its
 // row of P^T: both are one thread's.
+// With a 16-bit cache P is rounded to the cache's type, as in the dense forward
+// (both operands of a kind::f16 product have one type): half a step of it per
+// probability.
+//
+// Measured (kernel and join, replayed from a graph; d 128, 32 query heads on 8 K/V
+// heads): 64 sequences of 820..8192 keys, one token, e4m3: 106 us for 611 MB (5.8
+// TB/s, 0.88 of a measured copy); 2 sequences of 105 to 131 thousand keys, 8
+// tokens, bf16 cache: 161 us for 1008 MB (6.3 TB/s, 0.96); 16 sequences of
+// 820..8192 keys, 32 tokens each (128 rows), e4m3: 109 us, the softmax's steps
+// (tensor core 23 % busy).
 //
 // Softmax.  A thread owns one key of a tile.  Rows keep a reference exponent r
 // (shared memory); probabilities are 2^(z - r), their sums per thread and
