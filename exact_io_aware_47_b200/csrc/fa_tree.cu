@@ -738,10 +738,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int pn = 0; pn < Lay::kPanels; ++pn)
             tma_load_3d(slots + slot * Lay::kSlotBytes + pn * 16384 + mine * p.box * 128, map,
                         &full[slot], pn * Lay::kPanelElems, cur.y, z);
-          if (E4M3 && !is_v) {                   // scales of both come with K
-            float* dst = reinterpret_cast<float*>(smem + Lay::kScale + loaded % Lay::kScales * 1024) + mine * p.box;
-            bulk_load(dst, p.c.k_scale + row, 4u * p.box, &full[slot]);
-            bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &full[slot]);
+          if constexpr (E4M3) {
+            if (!is_v) {                         // scales of both come with K
+              float* dst = reinterpret_cast<float*>(smem + Lay::kScale + loaded % Lay::kScales * 1024) + mine * p.box;
+              bulk_load(dst, p.c.k_scale + row, 4u * p.box, &full[slot]);
+              bulk_load(dst + 128, p.c.v_scale + row, 4u * p.box, &full[slot]);
+            }
           }
         }
         ++loaded;
