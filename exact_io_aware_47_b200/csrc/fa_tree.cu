@@ -41,7 +41,14 @@
 // column stay in registers until the end of the item.  r follows a row's
 // maximum only when a score passes it by a factor of 2^4 (2^8 for 16-bit P):
 // the usual tile needs no maximum at all, only one vote of the 128 threads
-// that no score did.  Two groups of 128 threads work at it.  Up to 32 rows they
+// that no score did.  With an 8-bit cache what is stored is p times the V scale,
+// and the reference follows that.  A row of zeros has the scale 1, some 2^9 times
+// its neighbours', and adds nothing, so it may not move a reference (the others'
+// probabilities would fall into the last steps of the terms): where a reference
+// is about to move, rows of scale 1 are looked through, and those of zeros count
+// as kTreeMinScale.  (Looked at for every row, it took 94.1 against 89.1 us for 64
+// sequences of 820..8192 keys at d = 64, for the wait and the reads of V at every
+// item's start; so 90.1 us.)  Two groups of 128 threads work at it.  Up to 32 rows they
 // take turns, a tile each, with references, sums and an O of their own that
 // meet at the item's end (two chains of dependent steps run at once: what a
 // tile costs with few rows is latency); from 64 rows on they share each tile,
@@ -78,6 +85,7 @@ static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, 
 // 123, 127 us.
 constexpr int kTreeItemCost = 4;
 constexpr float kTreeMinScale = 0x1p-90f;  // V scales below count as this (keeps sums in range)
+constexpr float kTreeMinScaleLog2 = -90.f;
 
 template <int D_, bool BF16, bool E4M3, int R_>
 struct TreeLayout {
@@ -477,6 +485,23 @@ __device__ __noinline__ void tree_add_not_finite(const TreeParams& p, int b, int
       }
     }
   }
+}
+
+// Whether the V row of key tid of tile i (8-bit cache) holds zeros only.  (The lanes
+// start at different 16-byte chunks: rows are 128 bytes apart.)
+template <class Lay>
+__device__ __forceinline__ bool tree_zero_row(const uint8_t* smem, int i, int tid) {
+  constexpr int kRowPanels = Lay::kConvert ? (Lay::D + 63) / 64 : 1;
+  const uint8_t* row = smem + tid * 128 +
+                       (Lay::kConvert ? Lay::kV16 + (i & 1) * Lay::kV16Bytes
+                                      : Lay::kV + i % Lay::kSlotsV * Lay::kSlotBytes);
+  uint32_t any = 0u;
+#pragma unroll
+  for (int c = 0; c < 8 * kRowPanels; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + (c >> 3) * 16384 + (((c + tid) & 7) << 4));
+    any |= v.x | v.y | v.z | v.w;
+  }
+  return (any & (Lay::kConvert ? 0x7FFF7FFFu : 0x7F7F7F7Fu)) == 0u;  // (signs apart)
 }
 
 // An item's Q, by WARPS warps of which this is number `worker` (four do 128 rows in
@@ -969,6 +994,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if constexpr (Lay::kConvert) return mbar_wait_warp(&v16_empty[i & 1], (i >> 1) & 1, wc, site);
       else return mbar_wait_warp(&kv_empty[kSlotsK + i % kSlotsV], (i / kSlotsV) & 1, wc, site);
     };
+    // V(i) is in shared memory, as the product reads it
+    auto wait_v = [&](int i, unsigned site) {
+      if constexpr (Lay::kConvert) return mbar_wait_warp(&v16_full[i & 1], (i >> 1) & 1, wc, site);
+      else return mbar_wait_warp(&kv_full[kSlotsK + i % kSlotsV], (i / kSlotsV) & 1, wc, site);
+    };
     TreeSeg seg;
     for (int si = 0; tree_next(walk, p, seg); ++si) {
       const int qb = si % Lay::kQBufs;
@@ -1104,6 +1134,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (threadIdx.x == 0) FA_TRACE_AT(i, 3);
         if (named_bar_or(bar_id, 128, top > kOver || force || !ok)) {
           // some row's reference moves (or a wait gave up)
+          if constexpr (E4M3) {
+            // rows of zeros, see the top; their scale is 1.  (O(i - kPBufs) is
+            // complete before V(i) is waited for, for the reason given below.)
+            const bool maybe = key < L && sv_now == 1.f;
+            if (__any_sync(0xffffffffu, maybe)) {
+              if (!Lay::kConvert && i >= Lay::kPBufs) ok = wait_o(i - Lay::kPBufs, 80) && ok;
+              ok = wait_v(i, 81) && ok;
+              if (ok && maybe && tree_zero_row<Lay>(smem, i, tid)) {
+                sv_now = 0.f;
+                lv = kTreeMinScaleLog2;
+              }
+            }
+          }
           if (!named_bar_and(bar_id, 128, ok)) { ok = false; break; }
           constexpr int kPart = kCols < 32 ? kCols : 32;  // (registers)
 #pragma unroll
@@ -1175,7 +1218,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // converted, that is done there)
         if (edge && !Lay::kConvert) {
           const int slot = i % kSlotsV;
-          ok = mbar_wait_warp(&kv_full[kSlotsK + slot], (i / kSlotsV) & 1, wc, 74) && ok;
+          ok = wait_v(i, 74) && ok;
           if (ok && u >= 0) {
             uint8_t* row = smem + Lay::kV + slot * Lay::kSlotBytes + tid * 128;
             // A thread has its key's row, or half of it if the groups share the

@@ -406,6 +406,11 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale
  *     the table are required; other values are clamped and reported.  With a
  *     bad page the results of its sequences are unspecified.  A V scale below
  *     2^-90 counts as 2^-90, one that is negative or infinite as NaN.
+ *   8-bit caches: a query's products p * v_scale are held to 2^-28 of the
+ *     largest of them, or of 2^-90 of its largest p if that is more.  Rows of
+ *     zeros (scale 1, as fa_cache_write leaves them) do not count there; for
+ *     all others a v_scale should be what the row's codes need, since one far
+ *     above it costs the other keys bits.
  *   workspace: fa_fwd_tree_workspace_size(B, Hq, Hk, T, d) bytes, 256-byte
  *     aligned; its contents on entry do not matter.  Calls that may overlap on
  *     the GPU need one each.

@@ -753,3 +753,115 @@ def test_training_with_rotary_positions(fa):
     assert (o.double().cpu() - ref).abs().max() <= O_MAX_ABS
     for got, want in zip((dq, dk, dv), grads):
         assert (got.double().cpu() - want).abs().max() <= GRAD_REL_MAX * want.abs().max()
+
+
+# --------------------------------------------------------------------------- scales of V rows
+
+class SinkTree(Tree):
+    """Bf16 or fp16 queries over an e4m3 cache whose key `at` of every head has
+    a score of `gap` (the others': about a normal distribution), zeros as its V
+    row unless `keep`, and V of standard deviation std elsewhere."""
+
+    def __init__(self, gap, std, at=(0,), keep=False, **kw):
+        super().__init__(e4m3=True, **kw)
+        rng = np.random.default_rng(99)
+        q = rng.standard_normal((self.B, self.Hq, self.T, self.d))
+        q[..., 0] = 8.0
+        self.q = torch.from_numpy(q).to(self.dtype).cuda()
+        for b in range(self.B):
+            L = self.ctx[b] + self.n[b]
+            for h in range(self.Hk):
+                k, v = rng.standard_normal((L, self.d)), std * rng.standard_normal((L, self.d))
+                k[:, 0] = 0.0
+                for j in at:
+                    k[j] = 0.0
+                    k[j, 0] = gap / (8.0 * self.scale)
+                    if not keep:
+                        v[j] = 0.0
+                self.put(b, h, k, v)
+
+    def put(self, b, h, k, v):
+        """K and V rows of one sequence and head, quantised into the cache."""
+        for store, cache, scale, x in ((self.keys, self.kc, self.ks, k), (self.values, self.vc, self.vs, v)):
+            codes, sc = quantize_rows(torch.from_numpy(x).to(self.dtype).float().numpy())
+            store[b, h] = dequantize_rows(codes, sc)
+            at = np.arange(len(x))
+            pages = self.table[b].numpy()[at // self.page]
+            cache.view(torch.uint8)[pages, h, at % self.page] = torch.from_numpy(codes).cuda()
+            scale[pages, h, at % self.page] = torch.from_numpy(sc).cuda()
+
+    def check_relative(self, o, lse, what="", absolute=0.0):
+        """As check(), with no absolute term beside the output type's own
+        smallest step (fp16's 2^-24; bf16's is far below all of these).
+        `absolute`: of a key, relative to the row's largest probability."""
+        half = _half(self.dtype)
+        least = 2.0 ** -25 if self.dtype == FP16 else 0.0
+        og, lg = f64(o), f64(lse)
+        for b in range(self.B):
+            m = np.asarray(self.mask)[b]
+            n, L = self.n[b], self.ctx[b] + self.n[b]
+            for h in range(self.Hq):
+                k, v = self.keys[b, h // (self.Hq // self.Hk)], self.values[b, h // (self.Hq // self.Hk)]
+                q = f64(self.q[b, h])[:n]
+                ro, rl, sp = ref_tree(q, k, v, self.ctx[b], m[:n], self.scale)
+                qk = (np.abs(q) @ np.abs(k).T).max(-1)
+                e = self.scale * (2.0 ** -17 * np.abs(q).max(-1) * np.abs(k).sum(-1).max()
+                                  + 2 * self.d * 2.0 ** -24 * qk) + 2.0 ** -21
+                tol = half * np.abs(ro) + (half + 4 * e + L * 2.0 ** -23)[:, None] * sp + least + L * absolute
+                err = np.abs(og[b, h, :n] - ro)
+                assert (err <= tol).all(), f"{what} b{b} h{h}: worst {(err / tol).max():.3g} times the tolerance"
+                ltol = 2 * e + L * 2.0 ** -23 + 2.0 ** -22 * np.abs(rl)
+                assert (np.abs(lg[b, h, :n] - rl) <= ltol).all(), \
+                    f"{what} b{b} h{h}: LSE {(np.abs(lg[b, h, :n] - rl) / ltol).max():.3g} times the tolerance"
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,group", [(1, 4), (8, 4), (16, 4), (32, 4)])
+def test_tree_zero_v_row_that_takes_the_weight(fa, dtype, d, T, group):
+    """A key whose V row is zero (stored with the scale 1) and whose score is far
+    above the others' takes weight and adds nothing; what the others add may not
+    be lost beside it."""
+    for gap, std in ((12.0, 0.1), (10.0, 0.01), (12.0, 0.01), (7.0, 1e-3), (0.0, 1e-3)):
+        c = SinkTree(gap, std, B=2, Hq=group, Hk=1, T=T, ctx=(3000, 900), d=d, page=64, dtype=dtype, seed=31)
+        o, lse = c.run(fa)
+        _ok(fa)
+        c.check_relative(o, lse, f"gap {gap} std {std}")
+
+
+@pytest.mark.parametrize("T", [1, 8, 16, 32])
+def test_tree_zero_v_rows_small_values_and_far_scores(fa, T):
+    """V far below one, zero rows in many places (a drafted one, all of a tile,
+    every third key), scores so far apart that the other keys count for 2^-87."""
+    kw = dict(B=1, Hq=4, Hk=1, T=T, ctx=(1500,), d=128, page=32, dtype=BF16, seed=32)
+    for gap, std, at in ((0.0, 1e-5, (0,)), (3.0, 1e-6, (700,)), (12.0, 0.01, (1500,)), (5.0, 0.01, range(128, 256)),
+                         (2.0, 0.01, range(0, 1500, 3)), (60.0, 0.1, (0,)), (60.0, 0.1, (900, 1400))):
+        c = SinkTree(gap, std, at=at, **kw)
+        o, lse = c.run(fa)
+        _ok(fa)
+        c.check_relative(o, lse, f"gap {gap} std {std} at {at}")
+
+
+@pytest.mark.parametrize("T", [1, 8, 16, 32])
+def test_tree_every_v_row_zero(fa, T):
+    c = SinkTree(3.0, 0.0, B=2, Hq=4, Hk=1, T=T, ctx=(1000, 5), d=128, page=32, dtype=BF16, seed=33)
+    o, lse = c.run(fa)
+    _ok(fa)
+    assert not o.any()
+    c.check_relative(o, lse, "zeros")
+
+
+@pytest.mark.parametrize("T", [1, 32])
+def test_tree_v_rows_of_scale_one(fa, T):
+    """Rows whose largest value is 448 have the scale of a row of zeros."""
+    for at, gap in (((), 0.0), ((0,), 12.0), ((0, 200), 3.0)):
+        c = SinkTree(gap, 0.1, at=at, B=1, Hq=4, Hk=1, T=T, ctx=(700,), d=128, page=32, dtype=BF16, seed=34)
+        rng = np.random.default_rng(35)
+        v = 40.0 * rng.standard_normal((c.ctx[0] + T, 128))
+        v[:, 3] = 448.0
+        v[list(at)] = 0.0
+        c.put(0, 0, c.keys[0, 0], v)
+        assert (c.vs[c.table[0].long().cuda(), 0].flatten()[:len(v)] == 1.0).all()
+        o, lse = c.run(fa)
+        _ok(fa)
+        c.check_relative(o, lse, f"at {at}")
