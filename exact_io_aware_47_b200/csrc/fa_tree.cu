@@ -84,7 +84,10 @@ static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, 
 // 114, 112 us; of 200..2000 keys 73, 54, 48, 48 us; 16 sequences, 128 rows, 159, 131,
 // 123, 127 us.
 constexpr int kTreeItemCost = 4;
-constexpr float kTreeMinScale = 0x1p-90f;  // V scales below count as this (keeps sums in range)
+// V scales below this move a reference as if they were this: it keeps sums, which
+// are without the scale, below 2^(90 + 15) a key.  (Their products keep their size,
+// and lose their last bits: 2^-28 x 2^-90 of the largest p is a step of the terms.)
+constexpr float kTreeMinScale = 0x1p-90f;
 constexpr float kTreeMinScaleLog2 = -90.f;
 
 template <int D_, bool BF16, bool E4M3, int R_>
@@ -1062,10 +1065,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const float* sc = reinterpret_cast<const float*>(smem + Lay::kScale + i % Lay::kScales * 1024);
             sk_now = sc[tid];
             sv_now = sc[128 + tid];
-            if (!(sv_now >= kTreeMinScale && sv_now < INFINITY))
-              sv_now = sv_now >= 0.f && sv_now < 1.f ? kTreeMinScale : NAN;
+            if (!(sv_now >= 0.f && sv_now < INFINITY)) sv_now = NAN;
           }
-          lv = lg2_approx(sv_now);
+          lv = lg2_approx(fmaxf(sv_now, kTreeMinScale));
         }
         // d: exponent of a probability against its row's reference (without
         // the V scale sv = 2^lv, which multiplies what is stored)

@@ -404,8 +404,8 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale
  *     and lse stay as they were.
  *   0 <= draft_lens[b] <= T and 0 <= ctx_lens[b] with ctx_lens[b] + n_b within
  *     the table are required; other values are clamped and reported.  With a
- *     bad page the results of its sequences are unspecified.  A V scale below
- *     2^-90 counts as 2^-90, one that is negative or infinite as NaN.
+ *     bad page the results of its sequences are unspecified.  A V scale
+ *     that is negative or infinite counts as NaN.
  *   8-bit caches: a query's products p * v_scale are held to 2^-28 of the
  *     largest of them, or of 2^-90 of its largest p if that is more.  Rows of
  *     zeros (scale 1, as fa_cache_write leaves them) do not count there; for

@@ -807,7 +807,11 @@ class SinkTree(Tree):
                 qk = (np.abs(q) @ np.abs(k).T).max(-1)
                 e = self.scale * (2.0 ** -17 * np.abs(q).max(-1) * np.abs(k).sum(-1).max()
                                   + 2 * self.d * 2.0 ** -24 * qk) + 2.0 ** -21
-                tol = half * np.abs(ro) + (half + 4 * e + L * 2.0 ** -23)[:, None] * sp + least + L * absolute
+                seen = np.ones((n, L), bool)
+                seen[:, self.ctx[b]:] = m[:n, :n] != 0
+                top = np.exp(np.where(seen, self.scale * (q @ k.T), -np.inf).max(-1) - rl)
+                tol = half * np.abs(ro) + (half + 4 * e + L * 2.0 ** -23)[:, None] * sp + least \
+                    + L * absolute * top[:, None]
                 err = np.abs(og[b, h, :n] - ro)
                 assert (err <= tol).all(), f"{what} b{b} h{h}: worst {(err / tol).max():.3g} times the tolerance"
                 ltol = 2 * e + L * 2.0 ** -23 + 2.0 ** -22 * np.abs(rl)
@@ -865,3 +869,27 @@ def test_tree_v_rows_of_scale_one(fa, T):
         o, lse = c.run(fa)
         _ok(fa)
         c.check_relative(o, lse, f"at {at}")
+
+
+@pytest.mark.parametrize("T", [1, 8, 16, 32])
+@pytest.mark.parametrize("std", [1e-28, 1e-29, 1e-31, 1e-33, 1e-37])
+def test_tree_v_rows_of_the_smallest_scales(fa, T, std):
+    """bf16 values down to the smallest that cache_write has a scale for (2^-126):
+    products p * v_scale are held to 2^-28 of the largest, or of 2^-90 of the
+    largest p (fa.h), and a code is at most 448."""
+    c = SinkTree(0.0, std, keep=True, B=1, Hq=4, Hk=1, T=T, ctx=(700,), d=128, page=32, dtype=BF16, seed=36)
+    assert (c.vs[c.table[0].long().cuda(), 0].flatten()[:700] < 2.0 ** -90).all()
+    o, lse = c.run(fa)
+    _ok(fa)
+    c.check_relative(o, lse, f"std {std}", absolute=448 * 2.0 ** -118)
+
+
+@pytest.mark.parametrize("T", [1, 32])
+def test_tree_a_v_scale_of_zero(fa, T):
+    """Codes times a scale of zero are zeros, like any other row of them."""
+    c = SinkTree(12.0, 0.01, keep=True, B=1, Hq=4, Hk=1, T=T, ctx=(700,), d=128, page=32, dtype=BF16, seed=37)
+    c.vs[c.table[0, 0].item(), 0, 0] = 0.0
+    c.values[0, 0][0] = 0.0
+    o, lse = c.run(fa)
+    _ok(fa)
+    c.check_relative(o, lse, "scale 0")
