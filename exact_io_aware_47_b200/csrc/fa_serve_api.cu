@@ -8,14 +8,16 @@ namespace {
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-// Strides of a [B, H, N, d] tensor: host int64[3] or nullptr for contiguous.
-int read_strides(const int64_t* s, int H, int N, int d, Strides3* out) {
+// Strides of a [B, H, N, d] tensor: host int64[3] or nullptr for contiguous.  No
+// dimension spans more than 2^40 elements, so extents stay far within 64 bits.
+int read_strides(const int64_t* s, int B, int H, int N, int d, Strides3* out) {
   if (s == nullptr) {
     *out = Strides3{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
     return FA_OK;
   }
+  const int n[3] = {B, H, N};
   for (int i = 0; i < 3; ++i)
-    if (s[i] < 0 || s[i] > (1ll << 40)) return FA_ERR_INVALID_ARG;
+    if (s[i] < 0 || s[i] > (1ll << 40) / std::max(n[i] - 1, 1)) return FA_ERR_INVALID_ARG;
   for (int i = 0; i < 3; ++i)
     if (s[i] % 8 != 0) return FA_ERR_ALIGNMENT;
   *out = Strides3{s[0], s[1], s[2]};
@@ -68,8 +70,8 @@ int rope_tensor(const void* x, const int64_t* xs, void* y, const int64_t* ys, in
   t->x = static_cast<const uint8_t*>(x);
   t->y = static_cast<uint8_t*>(y);
   t->heads = H;
-  if ((st = read_strides(xs, H, N, d, &t->xs)) != FA_OK) return st;
-  if ((st = read_strides(ys, H, N, d, &t->ys)) != FA_OK) return st;
+  if ((st = read_strides(xs, B, H, N, d, &t->xs)) != FA_OK) return st;
+  if ((st = read_strides(ys, B, H, N, d, &t->ys)) != FA_OK) return st;
   if (rows_may_overlap(t->ys, B, H, N, d)) return FA_ERR_INVALID_ARG;
   t->in_place = same_view(x, t->xs, y, t->ys, B, H, N);
   if (!t->in_place &&
@@ -221,8 +223,8 @@ extern "C" int fa_cache_write(const void* k, const int64_t* k_strides, const voi
   if (!aligned(k, 16) || !aligned(v, 16) || (start && !aligned(start, 4)) ||
       (lens && !aligned(lens, 4)))
     return FA_ERR_ALIGNMENT;
-  if ((st = read_strides(k_strides, Hk, N, d, &p.ks)) != FA_OK) return st;
-  if ((st = read_strides(v_strides, Hk, N, d, &p.vs)) != FA_OK) return st;
+  if ((st = read_strides(k_strides, B, Hk, N, d, &p.ks)) != FA_OK) return st;
+  if ((st = read_strides(v_strides, B, Hk, N, d, &p.vs)) != FA_OK) return st;
   p.k = static_cast<const uint8_t*>(k);
   p.v = static_cast<const uint8_t*>(v);
   p.start = start;

@@ -321,7 +321,8 @@ size_t fa_bwd_noalloc_max_bytes(void);
  *   fa_rope_bwd is the gradient: dx from dy, the same with -theta.
  *   q, k: two tensors of B, N, d rotated by one launch, with Hq and Hk heads;
  *     k may be NULL with Hk = 0.  *_strides: three host int64 (batch, head,
- *     row) in elements, each >= 0 and a multiple of 8, NULL for contiguous [B, H, N, d]; d
+ *     row) in elements, each >= 0 and a multiple of 8, no dimension spanning
+ *     more than 2^40 elements, NULL for contiguous [B, H, N, d]; d
  *     is contiguous.  Two rows of an output must not share memory.  An output
  *     is its input (same pointer and strides) or overlaps neither input.
  *   positions: device int32; row n of batch b is at

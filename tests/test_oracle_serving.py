@@ -267,3 +267,27 @@ def test_binding_refuses_what_the_library_cannot_see():
         fa.cache_read(None, cache, [0, 0], 4)
     with pytest.raises(ValueError):
         fa.cache_read(cache, cache, None, 4)
+
+
+def test_strides_that_span_more_than_any_memory(lib):
+    """A batch of 2^24 rows 2^40 elements apart would wrap around 64 bits.  (The
+    calls have a rot of 24, or V rows 4 elements apart, which is looked at later:
+    the strides alone decide between the two answers.)"""
+    from exact_io_aware_47_b200 import _lib
+
+    def rope(B, H, N, strides):
+        return lib.fa_rope(P, strides, P, strides, H, None, None, None, None, 0, None, 0, P, B, N, 64, 24, 0,
+                           1.0, 0, None)
+    I, U = _lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_UNSUPPORTED
+    assert rope(1 << 24, 1, 1, _i64(1 << 40, 64, 64)) == I
+    assert rope(1, 1 << 24, 1, _i64(64, 1 << 39, 64)) == I
+    assert rope(2, 2, 1 << 20, _i64(1 << 30, 1 << 31, 1 << 21)) == I
+    assert rope(2, 1, 1, _i64(1 << 40, 64, 64)) == U           # one step of 2^40
+    assert rope(1, 1, 1, _i64(1 << 40, 1 << 40, 1 << 40)) == U  # no step at all
+    assert rope(2, 4, 8, None) == U
+
+    def write(strides):
+        return lib.fa_cache_write(P, strides, P, _i64(0, 0, 4), 2 * P, 3 * P, None, None, P, 1, None, None,
+                                  1 << 24, 1, 1, 64, 4, 16, 0, 0, None)
+    assert write(_i64(1 << 40, 64, 64)) == I
+    assert write(_i64(1 << 16, 64, 64)) == _lib.FA_ERR_ALIGNMENT   # V's
