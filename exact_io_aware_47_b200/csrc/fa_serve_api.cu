@@ -61,6 +61,68 @@ bool ranges_overlap(const void* x, long long nx, const void* y, long long ny) {
   return a < b + 2 * ny && b < a + 2 * nx;
 }
 
+// Whether a row of x [B, Hx, N, d] can share memory with one of y [B, Hy, N, d].
+// Q, K and V are often slices of one buffer, so address ranges say little: with
+// the strides equal, or nearly so, row y - row x = y - x + sum of t_i s_i, where
+// t_i is the difference of two indices (of equal strides together), and the rows
+// meet if that is within (-d, d).  The largest stride first, each t_i has few
+// values from which the smaller strides can still get there; where a search of
+// kSteps does not end (strides that no tensor of separate rows has), the answer
+// is yes.
+struct RowDistance {
+  static constexpr int kSteps = 20000;
+  struct Term {
+    long long stride, lo, hi;  // t_i stride with lo <= t_i <= hi
+  };
+  Term term[6];
+  int terms = 0, steps = 0;
+  long long d;
+
+  void add(long long stride, long long lo, long long hi) {
+    if (stride == 0 || lo == hi) return;
+    int i = 0;
+    while (i < terms && term[i].stride > stride) ++i;
+    if (i == terms || term[i].stride != stride) {
+      for (int j = terms++; j > i; --j) term[j] = term[j - 1];
+      term[i] = Term{stride, 0, 0};
+    }
+    term[i].lo += lo;
+    term[i].hi += hi;
+  }
+  bool reaches(int i, long long at) {
+    if (i == terms) return -d < at && at < d;
+    long long least = at, most = at;  // of what the smaller strides can add
+    for (int j = i + 1; j < terms; ++j) {
+      least += term[j].lo * term[j].stride;
+      most += term[j].hi * term[j].stride;
+    }
+    const Term& c = term[i];
+    // least + t s < d and most + t s > -d
+    auto floor_div = [](long long a, long long b) { return a / b - (a % b < 0 ? 1 : 0); };
+    const long long lo = std::max(c.lo, floor_div(-d - most, c.stride) + 1);
+    const long long hi = std::min(c.hi, floor_div(d - 1 - least, c.stride));
+    for (long long t = lo; t <= hi; ++t) {
+      if (++steps > kSteps) return true;
+      if (reaches(i + 1, at + t * c.stride)) return true;
+    }
+    return false;
+  }
+};
+bool rows_may_meet(const void* x, const Strides3& xs, int Hx, const void* y, const Strides3& ys, int Hy,
+                   int B, int N, int d) {
+  if (!ranges_overlap(x, extent(xs, B, Hx, N, d), y, extent(ys, B, Hy, N, d))) return false;
+  RowDistance r;
+  r.d = d;
+  const long long x_st[3] = {xs.b, xs.h, xs.n}, y_st[3] = {ys.b, ys.h, ys.n};
+  const int nx[3] = {B, Hx, N}, ny[3] = {B, Hy, N};
+  for (int i = 0; i < 3; ++i) {
+    r.add(x_st[i], 1 - nx[i], 0);
+    r.add(y_st[i], 0, ny[i] - 1);
+  }
+  const auto bytes = static_cast<long long>(reinterpret_cast<intptr_t>(y) - reinterpret_cast<intptr_t>(x));
+  return r.reaches(0, bytes / 2);
+}
+
 int rope_tensor(const void* x, const int64_t* xs, void* y, const int64_t* ys, int B, int H, int N,
                 int d, int dtype, RopeTensor* t) {
   if (!x || !y) return FA_ERR_INVALID_ARG;
@@ -96,7 +158,10 @@ int rope_core(const void* q, const int64_t* qs, void* qo, const int64_t* qos, in
   } else {
     st = rope_tensor(k, ks, ko, kos, B, Hk, N, d, dtype, &p.t[1]);
     if (st != FA_OK) return st;
-    if (qo == ko || static_cast<const void*>(qo) == k || static_cast<const void*>(ko) == q)
+    const RopeTensor &tq = p.t[0], &tk = p.t[1];
+    if (rows_may_meet(qo, tq.ys, Hq, ko, tk.ys, Hk, B, N, d) ||
+        rows_may_meet(qo, tq.ys, Hq, k, tk.xs, Hk, B, N, d) ||
+        rows_may_meet(q, tq.xs, Hq, ko, tk.ys, Hk, B, N, d))
       return FA_ERR_INVALID_ARG;
   }
   if (rot < 16 || rot > d || rot % 16 != 0) return FA_ERR_UNSUPPORTED;

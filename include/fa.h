@@ -324,7 +324,9 @@ size_t fa_bwd_noalloc_max_bytes(void);
  *     row) in elements, each >= 0 and a multiple of 8, no dimension spanning
  *     more than 2^40 elements, NULL for contiguous [B, H, N, d]; d
  *     is contiguous.  Two rows of an output must not share memory.  An output
- *     is its input (same pointer and strides) or overlaps neither input.
+ *     is its input (same pointer and strides) or lies outside its address
+ *     range; q_out shares no row's memory with k and k_out, nor k_out with q
+ *     (slices of one buffer are fine).
  *   positions: device int32; row n of batch b is at
  *     positions[b * positions_stride + n] (positions_stride >= 0; 0: shared
  *     by the batch); NULL: p = n.  Any int32 value, in any order.

@@ -893,3 +893,24 @@ def test_tree_a_v_scale_of_zero(fa, T):
     o, lse = c.run(fa)
     _ok(fa)
     c.check_relative(o, lse, "scale 0")
+
+
+# --------------------------------------------------------------------------- memory that is shared
+
+def test_rope_in_place_inside_one_projection_per_head(fa):
+    """Q, K and V of a head side by side: address ranges overlap, rows do not."""
+    torch.manual_seed(41)
+    B, N, H, d = 2, 19, 3, 64
+    buf = torch.randn(B, N, H, 3, d).to(BF16).cuda()
+    q, k, v = (buf[:, :, :, i].transpose(1, 2) for i in range(3))
+    f = fa.rope_frequencies(d)[0].cuda()
+    want = fa.rope(q.contiguous(), k.contiguous(), f)
+    before = v.clone()
+    fa.rope(q, k, f, q_out=q, k_out=k)
+    _ok(fa)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, before)
+    from exact_io_aware_47_b200 import _lib
+    kept = buf.clone()
+    with pytest.raises(_lib.FAError):                       # Q's output begins inside K's first row
+        fa.rope(q.contiguous(), k, f, q_out=buf.view(-1)[d + 8:][:B * H * N * d].view(B, H, N, d), k_out=k)
+    assert torch.equal(buf, kept)

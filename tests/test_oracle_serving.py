@@ -291,3 +291,67 @@ def test_strides_that_span_more_than_any_memory(lib):
                                   1 << 24, 1, 1, 64, 4, 16, 0, 0, None)
     assert write(_i64(1 << 40, 64, 64)) == I
     assert write(_i64(1 << 16, 64, 64)) == _lib.FA_ERR_ALIGNMENT   # V's
+
+
+def _shares(x, xs, nx, y, ys, ny, d):
+    """Whether any element of two views is the same, by writing all of them down."""
+    def elements(at, st, n):
+        rows = (at + st[0] * np.arange(n[0])[:, None, None] + st[1] * np.arange(n[1])[:, None]
+                + st[2] * np.arange(n[2]))
+        return set((rows[..., None] + np.arange(d)).ravel().tolist())
+    return bool(elements(x, xs, nx) & elements(y, ys, ny))
+
+
+def test_rope_outputs_of_q_that_share_memory_with_k(lib):
+    """Every case is one that the checks before accept; a rot of 24 is refused
+    after them, so that no call gets further."""
+    from exact_io_aware_47_b200 import _lib
+    I, U = _lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_UNSUPPORTED
+    B, N, d, far = 2, 3, 64, 1 << 24
+
+    def rope(qo, qos, Hq, k, ks, ko, kos, Hk, q=None, qs=None):
+        """Places in elements; q of its own memory unless given."""
+        at = lambda e: P + 2 * e
+        return lib.fa_rope(P + far if q is None else at(q), _i64(*(qos if qs is None else qs)), at(qo), _i64(*qos),
+                           Hq, at(k), _i64(*ks), at(ko), _i64(*kos), Hk, None, 0, P, B, N, d, 24, 0, 1.0, 0, None)
+
+    # one buffer of a projection, in place: heads side by side, and per head
+    for W, sh, qat, kat, Hq, Hk in ((6 * d, d, 0, 4 * d, 4, 2), (6 * d, d, 2 * d, 0, 4, 2), (6 * d, 3 * d, 0, d, 2, 2),
+                                    (8 * d, 2 * d, d, 0, 4, 4)):
+        st = (N * W, sh, W)
+        assert rope(qat, st, Hq, kat, st, kat, st, Hk, q=qat) == U
+    st = (N * 6 * d, d, 6 * d)
+    other = (N * 9 * d, 3 * d, 9 * d)
+    assert rope(0, st, 4, 3 * d, st, 3 * d, st, 2, q=0) == I             # K's first head is Q's last
+    assert rope(0, st, 4, 5 * d, st, 5 * d, st, 2, q=0) == I             # K's second head is the next row's first of Q
+    assert rope(0, other, 3, d + 8, other, d + 8, other, 2, q=0) == U    # rows 0 .. 63 and 72 .. 135 of 192
+    assert rope(0, other, 3, d - 8, other, d - 8, other, 2, q=0) == I    # and 56 .. 119
+    contiguous = (4 * N * d, N * d, d)
+    assert rope(1 << 20, contiguous, 4, 0, contiguous, 1 << 21, contiguous, 4) == U
+    assert rope(64, contiguous, 4, 0, contiguous, 1 << 21, contiguous, 4) == I     # q_out in K
+    assert rope(1 << 20, contiguous, 4, 0, contiguous, (1 << 20) + 64, contiguous, 4) == I  # in k_out
+    qs = (4 * N * d, N * d, d)
+    assert rope(1 << 20, qs, 4, 0, contiguous, 1 << 21, contiguous, 4, q=(1 << 21) + 64) == I  # k_out in Q
+    # any strides and places, against all elements written down
+    rng = np.random.default_rng(7)
+    answers = {I: 0, U: 0}
+    for _ in range(400):
+        Hq, Hk = int(rng.integers(1, 4)), int(rng.integers(1, 4))
+
+        def strides(H):
+            dims, n, span = rng.permutation(3), (B, H, N), d
+            st = [0, 0, 0]
+            for i in dims:
+                st[i] = span + 8 * int(rng.integers(0, 2)) * int(rng.integers(0, 9))
+                span = st[i] * n[i]
+            return tuple(st)
+        qst, kst = strides(Hq), strides(Hk)
+        if rng.random() < 0.6:
+            kst = qst if Hk <= Hq else kst
+            qst = qst if Hk <= Hq else kst
+        qat, kat = 8 * int(rng.integers(0, 120)), 8 * int(rng.integers(0, 120))
+        want = I if _shares(qat, qst, (B, Hq, N), kat, kst, (B, Hk, N), d) else U
+        got = rope(qat, qst, Hq, kat, kst, kat, kst, Hk, q=qat)
+        assert got == want, (qat, qst, Hq, kat, kst, Hk)
+        answers[got] += 1
+    assert min(answers.values()) > 30
