@@ -29,6 +29,8 @@ from . import _lib
 from .attention import _DTYPES, _E4M3, _check_inputs, _on_device
 
 _I64x3 = ctypes.c_int64 * 3
+_INT32 = torch.iinfo(torch.int32)
+_WIDE = (torch.int64, torch.uint32, torch.uint64)   # integers past int32
 _functions = {}      # the library's functions by name
 
 
@@ -111,13 +113,25 @@ def _check(name, t, shape, dtype, device):
 
 def _int32_arg(name, x, shape, device, other=None):
     """Device int32 tensor of the shape (or the other one); lists and host
-    tensors are copied."""
+    tensors are copied, and refused where a value does not fit.  Device tensors of
+    wider integers are converted without a look at them from the host: values that
+    do not fit become the nearest that do."""
     if x is None:
         return None
     if not (torch.is_tensor(x) and x.is_cuda and x.dtype == torch.int32 and x.device == device
             and x.is_contiguous()):
         _on_device(name, x, device)
-        x = torch.as_tensor(x, dtype=torch.int32).to(device).contiguous()
+        x = torch.as_tensor(x)
+        if x.numel() and (x.is_floating_point() or x.is_complex() or x.dtype == torch.bool):
+            raise ValueError(f"{name} has dtype {x.dtype}, expected integers")
+        if x.dtype in _WIDE:
+            x = x.to(torch.int64)
+            low, high = _INT32.min, _INT32.max
+            if x.device.type != "cpu":
+                x = x.clamp(low, high)
+            elif x.numel() and not low <= int(x.min()) <= int(x.max()) <= high:
+                raise ValueError(f"{name} has values outside int32")
+        x = x.to(device, torch.int32).contiguous()
     if x.shape != shape and (other is None or x.shape != other):
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}"
                          + ("" if other is None else f" or {tuple(other)}"))
@@ -204,6 +218,10 @@ def rope(q, k, inv_freq, positions=None, interleaved=False, factor=1.0, q_out=No
     (2 i, 2 i + 1) if interleaved, else (i, i + rot / 2).  positions: int32 [N]
     or [B, N] (packed: [T]); None: 0 .. N - 1.  q_out, k_out: where the result
     goes (any strides; q and k themselves rotate in place), else new tensors.
+
+    Here and below, int32 arguments may be lists, host tensors or device tensors
+    of other integer types too.  Values that do not fit are refused on the host
+    and become the nearest that fit on the device (no call waits for the GPU).
     """
     return _rope("fa_rope", q, k, inv_freq, positions, interleaved, factor, q_out, k_out)
 

@@ -914,3 +914,37 @@ def test_rope_in_place_inside_one_projection_per_head(fa):
     with pytest.raises(_lib.FAError):                       # Q's output begins inside K's first row
         fa.rope(q.contiguous(), k, f, q_out=buf.view(-1)[d + 8:][:B * H * N * d].view(B, H, N, d), k_out=k)
     assert torch.equal(buf, kept)
+
+
+def test_wide_integers_on_the_device(fa):
+    """int64 device tensors: the same results, and a value past int32 is told as
+    out of range instead of being taken for a small one."""
+    from exact_io_aware_47_b200 import _lib
+    torch.manual_seed(42)
+    q = torch.randn(2, 2, 5, 64).to(BF16).cuda()
+    f = fa.rope_frequencies(64)[0].cuda()
+    pos = torch.randint(0, 1 << 20, (2, 5)).cuda()
+    a, b = (fa.rope(q, None, f, positions=p)[0] for p in (pos, pos.to(torch.int32)))
+    assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        fa.rope(q, None, f, positions=pos / 2)
+    with pytest.raises(ValueError):
+        fa.rope(q, None, f, positions=(pos / 2).cpu())
+    c = Tree(B=2, Hq=2, Hk=1, T=2, ctx=(30, 20), d=64, page=16, dtype=BF16, seed=43)
+    good = c.run(fa)
+    ctx, mask = torch.tensor(c.ctx).cuda(), torch.as_tensor(c.mask).cuda()
+
+    def run(ctx, table=c.table.cuda().long()):
+        return fa.forward_tree(c.q, c.kc, c.vc, ctx, tree_mask=mask, block_table=table, k_scale=c.ks, v_scale=c.vs)
+    got = run(ctx)
+    _ok(fa)
+    assert torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
+    got = run(ctx + torch.tensor([1 << 32, 0]).cuda())      # 30 if it wrapped
+    assert fa.device_status()[0] == _lib.FA_ERR_DEVICE_SEQLEN
+    assert torch.equal(got[0][1], good[0][1])
+    with pytest.raises(ValueError):
+        run([30 + (1 << 32), 20])
+    with pytest.raises(ValueError):
+        run([30.0, 20.0])
+    with pytest.raises(ValueError):
+        run(ctx, c.table.cuda().float())

@@ -355,3 +355,27 @@ def test_rope_outputs_of_q_that_share_memory_with_k(lib):
         assert got == want, (qat, qst, Hq, kat, kst, Hk)
         answers[got] += 1
     assert min(answers.values()) > 30
+
+
+@pytest.mark.parametrize("x", [[1.0, 2.0], [0, 1.5], np.array([1.0, 2.0]), torch.tensor([1.0, 2.0]),
+                               torch.tensor([1.0, 2.0], dtype=torch.float16), torch.tensor([True, False]),
+                               torch.tensor([1j, 2j]), [0, 2 ** 31], [-2 ** 31 - 1, 0],
+                               torch.tensor([0, 1 << 32]), np.array([1 << 40, 0]), [0, 1 << 70]])
+def test_integer_arguments_are_neither_cut_nor_wrapped(x):
+    """Positions p / factor would be cut to whole ones, 2^32 would become 0."""
+    from exact_io_aware_47_b200.serving import _int32_arg
+    with pytest.raises(ValueError):
+        _int32_arg("positions", x, (2,), torch.device("cpu"))
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.uint8, torch.int16, torch.uint16, torch.int32, torch.uint32,
+                                   torch.int64])
+def test_integer_arguments_of_other_types(dtype):
+    from exact_io_aware_47_b200.serving import _int32_arg
+    want = torch.tensor([1, 100], dtype=torch.int32)
+    for x in (torch.tensor([1, 100], dtype=dtype), torch.tensor([1, 100], dtype=dtype).numpy(), [1, 100]):
+        got = _int32_arg("lens", x, (2,), torch.device("cpu"))
+        assert got.dtype == torch.int32 and torch.equal(got, want)
+    assert _int32_arg("lens", [-2 ** 31, 2 ** 31 - 1], (2,), torch.device("cpu")).tolist() == [-2 ** 31, 2 ** 31 - 1]
+    with pytest.raises(ValueError):
+        _int32_arg("lens", [1, 2, 3], (2,), torch.device("cpu"))
