@@ -28,6 +28,7 @@ FA_FP16 = 1
 
 FA_CACHE_16 = 0
 FA_CACHE_E4M3 = 1
+FA_CACHE_CLEAR = 16
 
 # exported symbol -> (restype, argtypes)
 _VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t

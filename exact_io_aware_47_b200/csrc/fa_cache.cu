@@ -176,7 +176,8 @@ template <int D, bool BF16, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const CacheCopyParams p) {
   constexpr int kLanes = CacheBlock<D>::kLanes;
   const CopyPart c = copy_part<D>(p);
-  if (c.n0 >= c.len) return;
+  const int clear_end = p.clear ? p.N : 0;       // rows below it are written in any case
+  if (c.n0 >= max(c.len, clear_end)) return;
   const int lane = threadIdx.x % kLanes, n1 = c.n0 + threadIdx.x / kLanes;
   long long slot[kCachePasses];
   copy_slots<D>(p, c, lane, n1, slot);
@@ -195,13 +196,16 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
   }
 #pragma unroll
   for (int e = 0; e < kCachePasses; ++e) {
-    if (slot[e] < 0) continue;
-    const long long row = (static_cast<long long>(c.b) * p.c.Hk + c.h) * p.N + n1 + e * CacheBlock<D>::kRows;
+    const int n = n1 + e * CacheBlock<D>::kRows;
+    if (slot[e] < 0 && n >= clear_end) continue;
+    const long long row = (static_cast<long long>(c.b) * p.c.Hk + c.h) * p.N + n;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      uint4 y;
-      if constexpr (E4M3) y = from_e4m3x8<BF16>(x[e][w], scale[e][w]);
-      else y = x[e][w];
+      uint4 y = make_uint4(0u, 0u, 0u, 0u);
+      if (slot[e] >= 0) {
+        if constexpr (E4M3) y = from_e4m3x8<BF16>(x[e][w], scale[e][w]);
+        else y = x[e][w];
+      }
       __stcs(reinterpret_cast<uint4*>((w ? p.v_out : p.k_out) + row * D * 2) + lane, y);
     }
   }

@@ -65,6 +65,7 @@ struct CacheCopyParams {
   const int32_t* start;      // nullptr: 0
   const int32_t* lens;       // nullptr: N
   int B, N;
+  bool clear;                // read: rows that are not read become zeros
 };
 
 struct TreeParams {

@@ -314,6 +314,8 @@ extern "C" int fa_cache_read(const void* k_cache, const void* v_cache, const flo
   if (st != FA_OK) return st;
   CacheCopyParams p;
   std::memset(&p, 0, sizeof(p));
+  p.clear = (format & FA_CACHE_CLEAR) != 0;
+  format &= ~FA_CACHE_CLEAR;
   st = cache_view(k_cache, v_cache, k_scale, v_scale, block_table, table_stride, B, Hk, d,
                   num_pages, page_size, format, &p.c);
   if (st != FA_OK) return st;

@@ -300,8 +300,9 @@ def cache_read(k_cache, v_cache, start, n, lens=None, block_table=None, k_scale=
                v_scale=None, dtype=None, k_out=None, v_out=None):
     """Rows start[b] .. start[b] + lens[b] - 1 of every sequence of the cache
     (start a tensor or list [B]; lens None: n) as ``(k, v)`` [B, Hk, n, d] in
-    ``dtype`` (default: the cache's, bfloat16 for e4m3).  Rows behind lens[b]
-    are left as they were in k_out, v_out, and are zero in new tensors."""
+    ``dtype`` (default: the cache's, bfloat16 for e4m3).  Rows behind lens[b] and
+    rows of bad positions are left as they were in k_out, v_out, and are zero in
+    new tensors."""
     if not torch.is_tensor(k_cache):
         raise ValueError("k_cache must be a CUDA tensor")
     if start is None:
@@ -317,7 +318,9 @@ def cache_read(k_cache, v_cache, start, n, lens=None, block_table=None, k_scale=
         raise ValueError("dtype must be bfloat16 or float16")
     if fmt == _lib.FA_CACHE_16 and dtype != k_cache.dtype:
         raise ValueError(f"a {k_cache.dtype} cache is read back as {k_cache.dtype}")
-    new = torch.empty if lens is None else torch.zeros
+    # new tensors are cleared by the kernel, beside one that is given by torch
+    both = k_out is None and v_out is None
+    new = torch.empty if both else torch.zeros
     k_out = new((B, Hk, n, d), dtype=dtype, device=dev) if k_out is None else k_out
     v_out = new((B, Hk, n, d), dtype=dtype, device=dev) if v_out is None else v_out
     _check("k_out", k_out, (B, Hk, n, d), dtype, dev)
@@ -326,7 +329,8 @@ def cache_read(k_cache, v_cache, start, n, lens=None, block_table=None, k_scale=
     lens = _int32_arg("lens", lens, (B,), dev)
     _launch("fa_cache_read", dev, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
             _ptr(v_scale), k_out.data_ptr(), v_out.data_ptr(), _ptr(table), stride, _ptr(start),
-            _ptr(lens), B, Hk, n, d, k_cache.shape[0], page, fmt, _DTYPES[dtype])
+            _ptr(lens), B, Hk, n, d, k_cache.shape[0], page, fmt | _lib.FA_CACHE_CLEAR if both else fmt,
+            _DTYPES[dtype])
     return k_out, v_out
 
 

@@ -374,10 +374,11 @@ int fa_rope_bwd(const void* dq, const int64_t* dq_strides, void* dq_in,
  * fa_cache_read: position start[b] + n to row n of k_out, v_out [B, Hk, N, d]
  *   (contiguous, 16-bit, `dtype`) for n < lens[b]: code * scale in fp32,
  *   rounded once.  Rows behind lens[b], and rows of bad positions, stay as
- *   they were.
+ *   they were, or become zeros if format is or-ed with FA_CACHE_CLEAR (for
+ *   outputs whose memory holds anything).
  *   0 <= lens[b] <= N is required.  B*Hk*N*d < 2^31; d in {64, 128}.
  */
-typedef enum { FA_CACHE_16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_format;
+typedef enum { FA_CACHE_16 = 0, FA_CACHE_E4M3 = 1, FA_CACHE_CLEAR = 16 } fa_cache_format;
 
 int fa_cache_write(const void* k, const int64_t* k_strides, const void* v,
                    const int64_t* v_strides, void* k_cache, void* v_cache, float* k_scale,

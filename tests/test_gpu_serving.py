@@ -948,3 +948,42 @@ def test_wide_integers_on_the_device(fa):
         run([30.0, 20.0])
     with pytest.raises(ValueError):
         run(ctx, c.table.cuda().float())
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_cache_read_leaves_no_row_of_a_new_tensor_unwritten(fa, e4m3, d):
+    """Rows behind lens, of positions past the table and of pages that are not in
+    the pool are zeros in new tensors, whatever their memory held; tensors that
+    the caller gives keep them."""
+    from exact_io_aware_47_b200 import _lib
+    B, Hk, page, N = 3, 2, 16, 150
+    per = 10
+    table = _table(B, per, B * per + 1, 44)
+    kc, vc, ks, vs = _pool(B * per + 1, Hk, page, d, BF16, e4m3)
+    g = torch.Generator(device="cuda").manual_seed(44)
+    k, v = (torch.randn(B, Hk, per * page, d, generator=g, device="cuda").to(BF16) for _ in range(2))
+    fa.cache_write(k, v, kc, vc, block_table=table.cuda(), k_scale=ks, v_scale=vs)
+    _ok(fa)
+    table[1, 3], table[2, 0] = B * per + 1, -1
+    t = table.cuda()
+    kw = dict(block_table=t, k_scale=ks, v_scale=vs)
+    whole = [torch.full((B, Hk, N, d), 3.0, dtype=BF16, device="cuda") for _ in range(2)]
+    for start, lens in (([0, 0, 0], None), ([140, 7, 3], None), ([0, 0, 0], [150, 60, 0]), ([30, 2, 0], [150, 149, 33]),
+                        ([0, 0, 2 ** 31 - 1], None), ([0, -3, 0], [0, 150, 150]), ([0, 0, 0], [-1, 200, 150])):
+        for x in whole:
+            x.fill_(3.0)
+        got = fa.cache_read(kc, vc, start, N, lens=lens, k_out=whole[0], v_out=whole[1], **kw)
+        assert fa.device_status()[0] == _lib.FA_ERR_DEVICE_SEQLEN
+        assert got[0] is whole[0]
+        junk = [torch.full((B, Hk, N, d), 7.0, dtype=BF16, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        del junk
+        new = fa.cache_read(kc, vc, start, N, lens=lens, **kw)
+        half = fa.cache_read(kc, vc, start, N, lens=lens, v_out=whole[1].clone(), **kw)
+        assert fa.device_status()[0] == _lib.FA_ERR_DEVICE_SEQLEN
+        for i in range(2):
+            kept = (whole[i] == 3.0).all(-1, keepdim=True)
+            assert kept.any() and not kept.all()
+            assert torch.equal(new[i], torch.where(kept, torch.zeros_like(new[i]), whole[i])), f"{start} {lens} {i}"
+        assert torch.equal(half[0], new[0]) and torch.equal(half[1], whole[1])

@@ -379,3 +379,20 @@ def test_integer_arguments_of_other_types(dtype):
     assert _int32_arg("lens", [-2 ** 31, 2 ** 31 - 1], (2,), torch.device("cpu")).tolist() == [-2 ** 31, 2 ** 31 - 1]
     with pytest.raises(ValueError):
         _int32_arg("lens", [1, 2, 3], (2,), torch.device("cpu"))
+
+
+def test_the_clearing_flag_belongs_to_reading(lib):
+    """Every call has a misaligned output or cache, looked at after the format."""
+    from exact_io_aware_47_b200 import _lib
+    I, A, clear = _lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_ALIGNMENT, _lib.FA_CACHE_CLEAR
+
+    def read(fmt):
+        return lib.fa_cache_read(P, 2 * P, P, 2 * P, 3 * P, 4 * P + 8, P, 4, None, None, 2, 2, 4, 64, 8, 16, fmt, 0, None)
+
+    def write(fmt):
+        return lib.fa_cache_write(P, None, P, None, P + 8, 2 * P, P, 2 * P, P, 4, None, None, 2, 2, 4, 64, 8, 16, fmt,
+                                  0, None)
+    for fmt in (0, 1):
+        assert read(fmt) == A and read(fmt | clear) == A and write(fmt) == A and write(fmt | clear) == I
+    for fmt in (2, -1, 32, 8, clear | 2):
+        assert read(fmt) == I
