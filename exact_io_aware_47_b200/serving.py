@@ -351,8 +351,9 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
     [T, T], or [B, T, T]; None: u <= t).  T = 1 is ordinary decoding.  Hq may be
     a multiple of the cache's Hk (shared K/V heads).  draft_lens [B]: how many
     of the T tokens a sequence has; rows behind them are left as they were in
-    out and lse, and are O = 0, LSE = -inf in new tensors.  Cache and
-    block_table as in ``cache_write``.
+    out and lse, and are O = 0, LSE = -inf in new tensors (as are tokens past the
+    positions of the table, which are reported).  Cache and block_table as in
+    ``cache_write``.
     """
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, T, d]")
@@ -371,11 +372,12 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
     if fmt == _lib.FA_CACHE_16 and k_cache.dtype != q.dtype:
         raise ValueError(f"q has dtype {q.dtype}, the cache {k_cache.dtype}")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    full = draft_lens is None and T <= stride * page     # every row has a result
     if out is None:
-        out = torch.empty_like(q) if draft_lens is None else torch.zeros_like(q)
+        out = torch.empty_like(q) if full else torch.zeros_like(q)
     if lse is None:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-        if draft_lens is not None:
+        if not full:
             lse.fill_(-math.inf)
     _check("out", out, shape, dt, dev)
     _check("lse", lse, (B, Hq, T), torch.float32, dev)

@@ -987,3 +987,22 @@ def test_cache_read_leaves_no_row_of_a_new_tensor_unwritten(fa, e4m3, d):
             assert kept.any() and not kept.all()
             assert torch.equal(new[i], torch.where(kept, torch.zeros_like(new[i]), whole[i])), f"{start} {lens} {i}"
         assert torch.equal(half[0], new[0]) and torch.equal(half[1], whole[1])
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_tree_leaves_no_row_of_a_new_tensor_unwritten(fa, e4m3):
+    """More drafted tokens than a sequence's table has positions: the last ones
+    have no key and no result, and the new tensors say so."""
+    from exact_io_aware_47_b200 import _lib
+    c = Tree(B=2, Hq=2, Hk=1, T=20, ctx=(0, 0), drafts=[16, 16], d=64, page=16, dtype=BF16, e4m3=e4m3, mask=None,
+             seed=45)
+    table = c.table[:, :1].contiguous().cuda()
+    want = c.run(fa, block_table=table)
+    _ok(fa)
+    junk = [torch.full((2, 2, 20, 64), 7.0, dtype=BF16, device="cuda"), torch.full((2, 2, 20), 7.0, device="cuda")]
+    torch.cuda.synchronize()
+    del junk
+    o, lse = c.run(fa, block_table=table, draft_lens=None)
+    assert fa.device_status()[0] == _lib.FA_ERR_DEVICE_SEQLEN
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert not o[:, :, 16:].any() and (lse[:, :, 16:] == -math.inf).all()
