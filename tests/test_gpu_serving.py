@@ -1006,3 +1006,77 @@ def test_tree_leaves_no_row_of_a_new_tensor_unwritten(fa, e4m3):
     assert fa.device_status()[0] == _lib.FA_ERR_DEVICE_SEQLEN
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert not o[:, :, 16:].any() and (lse[:, :, 16:] == -math.inf).all()
+
+
+# --------------------------------------------------------------------------- drafted values that are not finite
+
+def _poisoned(fa, dtype, e4m3, d, T, group, ctx, Hk, value, chain, page=32, drafts=None):
+    """The batch twice: clean, and with one element of V that is not finite in one
+    drafted token of every third sequence and head.  Queries that do not see the
+    token keep every bit, those that see it all columns but the element's."""
+    B, Hq = len(ctx), Hk * group
+    g = torch.Generator(device="cuda").manual_seed(T + d + B)
+    n = torch.tensor([T] * B if drafts is None else drafts, device="cuda")
+    c = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+    per = (max(ctx) + T + page - 1) // page
+    table = torch.randperm(B * per, generator=g, device="cuda").view(B, per).to(torch.int32)
+    kc, vc, ks, vs = _pool(B * per, Hk, page, d, dtype, e4m3)
+    k, v = (torch.randn(B, Hk, max(ctx) + T, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    fa.cache_write(k, v, kc, vc, lens=(c + n).to(torch.int32), block_table=table, k_scale=ks, v_scale=vs)
+    q = torch.randn(B, Hq, T, d, generator=g, device="cuda").to(dtype)
+    mask = torch.ones(T, T, device="cuda").tril()
+    if not chain:
+        mask = mask * (torch.rand(T, T, generator=g, device="cuda") < 0.5)
+        mask.fill_diagonal_(1)                               # (a token sees itself: some query sees each)
+    mask = mask.to(torch.uint8)
+    kw = dict(draft_lens=None if drafts is None else n.to(torch.int32), tree_mask=None if chain else mask,
+              block_table=table, k_scale=ks, v_scale=vs)
+    clean, clean_lse = fa.forward_tree(q, kc, vc, c, **kw)
+    _ok(fa)
+    assert torch.isfinite(clean).all()
+    raw = vc.view(torch.uint8) if e4m3 else vc
+    hit = torch.zeros(B, Hq, T, d, dtype=torch.bool, device="cuda")
+    for b in range(0, B, 3):
+        for h in range(b % 2, Hk, 2):
+            u, col = (5 * b + 7 * h) % max(1, int(n[b])), (11 * b + 17 * h + 3) % d
+            if u >= int(n[b]):
+                continue
+            j = ctx[b] + u
+            raw[int(table[b, j // page]), h, j % page, col] = 0x7F + 0x80 * (b % 2) if e4m3 else value
+            sees = (mask[:, u] != 0) & (torch.arange(T, device="cuda") < n[b])
+            hit[b, h * group:(h + 1) * group, :, col] |= sees
+    assert hit.any() and not hit.all()
+    o, lse = fa.forward_tree(q, kc, vc, c, **kw)
+    _ok(fa)
+    assert torch.equal(lse, clean_lse)
+    got = o[hit]
+    if e4m3 or math.isnan(value):
+        assert torch.isnan(got).all(), f"{int((~torch.isnan(got)).sum())} of {got.numel()} lost"
+    else:
+        assert (got == value).all(), f"{int((got != value).sum())} of {got.numel()} lost"
+    assert torch.equal(o[~hit], clean[~hit]), f"{int((o[~hit] != clean[~hit]).sum())} reached others"
+
+
+_NOT_FINITE = [(BF16, True, math.nan), (FP16, True, math.nan), (BF16, False, math.nan), (FP16, False, math.inf),
+               (BF16, False, -math.inf), (FP16, False, math.nan)]
+
+
+@pytest.mark.parametrize("dtype,e4m3,value", _NOT_FINITE)
+@pytest.mark.parametrize("T,group", [(1, 8), (2, 4), (8, 4), (16, 4), (33, 4), (130, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_drafted_values_that_are_not_finite(fa, dtype, e4m3, value, T, group, d):
+    """Every tile of rows, drafted tokens on either side of a tile's edge, short
+    and long contexts (whose items are cut over many CTAs), with and without masks."""
+    for chain in (True, False) if T > 1 else (True,):
+        _poisoned(fa, dtype, e4m3, d, T, group, [30, 0, 120, 4000], 2, value, chain)
+        _poisoned(fa, dtype, e4m3, d, T, group, [9000], 1, value, chain, page=48)
+    if T > 2:
+        _poisoned(fa, dtype, e4m3, d, T, group, [125, 40, 0, 500], 2, value, False, drafts=[T - 1, 0, T, T // 2])
+
+
+@pytest.mark.parametrize("dtype,e4m3,value", _NOT_FINITE)
+@pytest.mark.parametrize("T,group", [(2, 4), (8, 4), (16, 4), (33, 4)])
+def test_tree_many_items_some_of_them_not_finite(fa, dtype, e4m3, value, T, group):
+    """Items of one to three tiles, about ten in a row per SM: what one of them
+    found may not be taken for another's."""
+    _poisoned(fa, dtype, e4m3, 128, T, group, [(37 * b) % 290 for b in range(400)], 4, value, False)
