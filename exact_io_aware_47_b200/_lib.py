@@ -203,28 +203,8 @@ def fa_fwd_e4m3(q8, k8, v8, q_descale, k_descale, v_descale, o, lse, B, H, N, d,
                               scale, causal, seqlens, out_dtype, stream)
 
 
-def fa_rope(*args):
-    return load().fa_rope(*args)
-
-
-def fa_rope_bwd(*args):
-    return load().fa_rope_bwd(*args)
-
-
-def fa_cache_write(*args):
-    return load().fa_cache_write(*args)
-
-
-def fa_cache_read(*args):
-    return load().fa_cache_read(*args)
-
-
 def fa_fwd_tree_workspace_size(B, Hq, Hk, T, d):
     return load().fa_fwd_tree_workspace_size(B, Hq, Hk, T, d)
-
-
-def fa_fwd_tree(*args):
-    return load().fa_fwd_tree(*args)
 
 
 def fa_bwd_noalloc_max_bytes():

@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     TreeSeg seg;
     const bool cont = tree_next(first, p, seg) && seg.t0 > 0;
     *reinterpret_cast<int4*>(p.heads + blockIdx.x * 4) =
-        cont ? make_int4(seg.b, seg.hk * p.row_tiles + seg.rt, seg.t1 == seg.nt, seg.drafts)
+        cont ? make_int4(seg.b, seg.hk * p.row_tiles + seg.rt, seg.drafts, 0)
              : make_int4(-1, -1, 0, 0);
   }
 
@@ -1469,7 +1469,7 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) fa_tree_join_kernel(const
   const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
   const int r = ways == 1 ? blockIdx.y * kTreeJoinWarps + warp : blockIdx.y;
   const int m = rt * R + r;
-  if (r >= R || m >= p.group * p.T || m % p.T >= head.w) return;  // (ways = 8: the whole block)
+  if (r >= R || m >= p.group * p.T || m % p.T >= head.z) return;  // (ways = 8: the whole block)
   const size_t slot_floats = static_cast<size_t>(R) * (D + 2);
   auto part = [&](int i) {
     return p.partial + (i == 0 ? 2 * static_cast<size_t>(c0 - 1) + 1 : 2 * static_cast<size_t>(c0 + i - 1)) * slot_floats;
