@@ -30,11 +30,13 @@
 // probability.
 //
 // Measured (kernel and join, replayed from a graph; d 128, 32 query heads on 8 K/V
-// heads): 64 sequences of 820..8192 keys, one token, e4m3: 106 us for 611 MB (5.8
-// TB/s, 0.88 of a measured copy); 2 sequences of 105 to 131 thousand keys, 8
-// tokens, bf16 cache: 161 us for 1008 MB (6.3 TB/s, 0.96); 16 sequences of
-// 820..8192 keys, 32 tokens each (128 rows), e4m3: 109 us, the softmax's steps
-// (tensor core 23 % busy).
+// heads): 64 sequences of 820..8192 keys, one token, e4m3: 108 us for 611 MB (5.7
+// TB/s, 0.87 of a measured copy); 2 sequences of 105 to 131 thousand keys, 8
+// tokens, bf16 cache: 160 us for 1008 MB (6.3 TB/s, 0.96); 16 sequences of
+// 820..8192 keys, 32 tokens each (128 rows), e4m3: 113 us, of which a CTA's 34
+// tiles take 69 (2.03 us, 3990 cycles at 1965 MHz, a tile: the softmax's steps in
+// this arrangement; tensor core 23 % busy) and the rest launch, items' starts and
+// ends and the join.
 //
 // Softmax.  A thread owns one key of a tile.  Rows keep a reference exponent r
 // (shared memory); probabilities are 2^(z - r), their sums per thread and
@@ -76,13 +78,19 @@ constexpr int kTreeThreads = 512;
 // Registers: 512 threads are launched with 128 each.  With 128 rows a softmax
 // thread holds 64 columns (scores and sums) and needs more: its warpgroups take
 // 176, the other two keep 80 (2 x 176 + 2 x 80 = 4 x 128; 16 sequences with 128
-// rows: 109 us, with 184 and 72 111, with 192 and 64 112).
+// rows: 113 us, with 184 and 72 116, with 192 and 64 116).
 constexpr int kTreeLaunchRegs = 128, kTreeSoftmaxRegs = 176, kTreeOtherRegs = 80;
 static_assert(2 * kTreeSoftmaxRegs + 2 * kTreeOtherRegs <= 4 * kTreeLaunchRegs, "register split");
-// What an item's start and end cost, in tiles, where the line of work is cut.
-// Cuts at 0, 2, 4, 7: 64 sequences of 820..8192 keys, one row tile of 16, 133, 118,
-// 114, 112 us; of 200..2000 keys 73, 54, 48, 48 us; 16 sequences, 128 rows, 159, 131,
-// 123, 127 us.
+// What an item's start and end cost, in tiles, where the line of work is cut.  One
+// number serves all kinds of tile, the best or within 8 % of it for each.  Counted
+// as 0, 2, 4, 7 (us; 32 query heads on 8, lengths from a tenth of the longest up):
+//   8-bit, d 128, 16 rows: 64 sequences to 8192 keys 118, 109, 108, 108
+//                          64 sequences to 2000 keys 67, 52, 46, 44
+//     32 rows, fp16: 64 to 4000   120, 101, 90, 85     64 rows: 32 to 4000  96, 83, 76, 77
+//     128 rows, fp16: 16 to 8192  134, 118, 113, 117
+//   8-bit, d 64, 16 rows: 64 to 8192  110, 99, 90, 84  32 rows: 64 to 4000  110, 92, 81, 76
+//   16-bit, d 128, 16 rows: 64 to 2000  65, 59, 60, 62  128 rows: 16 to 8192  112, 100, 95, 93
+//   16-bit, d 64, 16 rows: 64 to 8192  113, 107, 106, 106
 constexpr int kTreeItemCost = 4;
 // V scales below this move a reference as if they were this: it keeps sums, which
 // are without the scale, below 2^(90 + 15) a key.  (Their products keep their size,

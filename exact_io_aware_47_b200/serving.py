@@ -353,7 +353,8 @@ def forward_tree(q, k_cache, v_cache, ctx_lens, draft_lens=None, tree_mask=None,
     of the T tokens a sequence has; rows behind them are left as they were in
     out and lse, and are O = 0, LSE = -inf in new tensors (as are tokens past the
     positions of the table, which are reported).  Cache and block_table as in
-    ``cache_write``.
+    ``cache_write``; a v_scale should be what its row's codes need, as there,
+    since one far above it costs the other keys bits.
     """
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, T, d]")
